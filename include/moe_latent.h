@@ -379,6 +379,137 @@ int moe_combine_norm_up_reap(const moe_shape *shape, int T, const float *Y, cons
                              int accumulate, const int32_t *expert_offsets, double *sal_sum, int64_t *counts,
                              int reap_accumulate, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- Around the layer: the norms of the decoder block, the dense products in
+ * 8 bits, and the layer itself for a few tokens.
+ *
+ * 8-bit activations: e4m3 codes (OCP, largest finite 448) with one scale per
+ * row and block of 128 consecutive values (the last block may be shorter).
+ * The scale is 2^(b - 127) for the stored byte b: the smallest power of two
+ * that keeps the block's largest magnitude within 448, b in 1..247 (1 for a
+ * block of zeros); values are rounded to nearest, ties to even.  A value that
+ * is not finite becomes the NaN code 0x7F and takes no part in its scale. */
+
+/* the forms in which a normed row is written */
+typedef struct {
+  const uint16_t *gamma; /* [H] bf16 */
+  uint16_t *n;           /* [T, ldn] bf16, or NULL */
+  int64_t ldn;           /* elements between rows, >= H */
+  uint8_t *q;            /* [T, ldq] e4m3 codes, or NULL (n, q or both) */
+  int64_t ldq;           /* >= H */
+  uint8_t *q_scale;      /* [T, ldqs] scale bytes, NULL exactly when q is */
+  int64_t ldqs;          /* >= H / 128 rounded up */
+} moe_norm_out;
+
+/* RMSNorm in front of a block:
+ *   n_t = x_t / sqrt(mean(x_t^2) + eps) * gamma,
+ * computed in fp32 and written as bf16 (the layer's input), as 8-bit codes
+ * with block scales (the 8-bit product's input; quantised from the fp32
+ * value), or both.
+ *   x   [T, ldx] fp32 or bf16 (MOE_DT_F32, MOE_DT_BF16)
+ * T may be 0.  Rows may have any width up to 16384 and any stride >= H: rows
+ * whose width is a multiple of 8 and that are 16-byte aligned (q: 8-byte) are
+ * moved in vectors, others value by value.  Outputs do not overlap x.
+ * Errors: MOE_EINVAL (bad size, dtype, stride, null or misaligned pointer);
+ * MOE_ENOTSUP (H > 16384). */
+int moe_block_pre_norm(int T, int H, const void *x, int x_dtype, int64_t ldx, float eps, const moe_norm_out *o,
+                       void *stream);
+
+/* gate of moe_block_post_norm */
+#define MOE_GATE_NONE 0
+#define MOE_GATE_TOKEN 1   /* one value per row: gate[t * ldg] */
+#define MOE_GATE_CHANNEL 2 /* one value per channel: gate[h] */
+#define MOE_GATE_FULL 3    /* one per value: gate[t * ldg + h] */
+
+typedef struct {
+  int32_t T, H;
+  const void *y;         /* [T, ldy] the block's output, fp32 or bf16 */
+  int64_t ldy;
+  const void *resid;     /* [T, ldr] the residual stream, `dtype` */
+  int64_t ldr;
+  void *out;             /* [T, ldo], `dtype`; may be resid itself (with ldo == ldr) */
+  int64_t ldo;
+  int32_t y_dtype, dtype;
+  const uint16_t *gamma; /* [H] bf16 weight of the norm after the block; NULL: no norm */
+  const void *gate;      /* per gate_kind, fp32 or bf16; NULL exactly for MOE_GATE_NONE */
+  int64_t ldg;           /* MOE_GATE_TOKEN: >= 1; MOE_GATE_FULL: >= H */
+  int32_t gate_kind, gate_dtype, gate_sigmoid; /* gate_sigmoid 1: the gate is sigmoid(value) */
+  float scale;           /* residual scale: multiplies the gated branch */
+  float eps;
+  const moe_norm_out *next; /* the next block's pre-norm, or NULL */
+} moe_post_norm_args;
+
+/* The norm after a block, its gate, the residual, and the norm in front of the
+ * next block, in one pass over the rows:
+ *   out_t  = resid_t + scale * g_t * (y_t / sqrt(mean(y_t^2) + eps) * gamma)
+ *   next_t = out_t / sqrt(mean(out_t^2) + eps) * next->gamma
+ * in fp32; out is rounded once to `dtype`, and next is taken from the rounded
+ * row, so it equals moe_block_pre_norm of out bit for bit.  Sizes, strides,
+ * alignment and errors as for moe_block_pre_norm; MOE_EINVAL also for an
+ * unknown gate_kind, or a gate without its kind. */
+int moe_block_post_norm(const moe_post_norm_args *a, void *stream);
+
+/* Rows of fp32 or bf16 values as 8-bit codes with block scales (above).
+ *   x [T, ldx], q [T, ldq], q_scale [T, ldqs]; T may be 0; any K.
+ * Errors: MOE_EINVAL. */
+int moe_fp8_quantize(int T, int K, const void *x, int x_dtype, int64_t ldx, uint8_t *q, int64_t ldq,
+                     uint8_t *q_scale, int64_t ldqs, void *stream);
+
+/* scales of the 8-bit product's weights */
+#define MOE_SCALE_F32 0  /* fp32 */
+#define MOE_SCALE_E8M0 1 /* byte b: 2^(b - 127); b = 255 is NaN */
+
+/* Dense product of 8-bit activations and 8-bit weights:
+ *   out[t, n] (+)= sum_b sx[t, b] sw[n / 128, b] sum_{k in block b} x[t, k] w[n, k]
+ *   x       [T, ldx]  e4m3 codes, ldx a multiple of 16
+ *   x_scale [T, ldxs] scale bytes per block of 128 of a row
+ *   w       [N, K]    e4m3 codes
+ *   w_scale [N / 128, K / 128], both rounded up: one scale per 128 x 128 block,
+ *           fp32 or e8m0 bytes
+ *   out     [T, ldo]  fp32 (written, or added to with accumulate = 1) or bf16
+ * fp32 out: products are exact and sums fp32.  bf16 out may use the 8-bit
+ * matrix instructions, which drop what lies some 14 bits below a group's
+ * largest product (1.5e-5 of the result's rms on normally distributed
+ * operands, a hundredth of the rounding to bf16); out is rounded once.
+ * x_scale bytes are 1..247 (moe_fp8_quantize's).  Deterministic.
+ * T may be 0; N is free; K is a multiple of 16 (else MOE_ENOTSUP; K up to 2^20,
+ * T, N and ldx up to 2^22).
+ * Workspace: moe_fp8_gemm_workspace_bytes(T, N, K) bytes (0: unsupported sizes).
+ * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */
+size_t moe_fp8_gemm_workspace_bytes(int T, int N, int K);
+int moe_fp8_gemm(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8_t *x_scale, int64_t ldxs,
+                 const uint8_t *w, const void *w_scale, int w_scale_type, void *out, int out_dtype, int64_t ldo,
+                 int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/* every weight of a layer, as the calls above take them */
+typedef struct {
+  const uint16_t *w_router; /* [E, H] bf16 */
+  const float *bias;        /* [E] */
+  const uint16_t *w_down;   /* [L, H] bf16 */
+  const uint8_t *w1_packed, *w1_scale, *w3_packed, *w3_scale, *w2_packed, *w2_scale;
+  const uint16_t *gamma;    /* [L] bf16 */
+  const uint16_t *w_up;     /* [H, L] bf16 */
+  const uint16_t *sh_gate, *sh_up, *sh_down; /* ignored without shared experts */
+} moe_layer_weights;
+
+/* The whole layer for up to MOE_FEW_MAX_T tokens, in two kernels: the results
+ * of moe_route, moe_permute, the two expert products, moe_combine_norm_up and
+ * shared_expert_ffn in one call.
+ *   x        [T, H] bf16
+ *   topk_ids [T, k] int32 and topk_w [T, k] fp32, or both NULL: the routing
+ *   out      [T, H] fp32
+ * The arithmetic is the layer's with activations that are not exact in bf16
+ * taken as three bf16 terms, so operand_mode has no effect: products see the
+ * fp32 values.  Selection and weights follow moe_route.  Deterministic.
+ * Calls on several streams at once are independent if their workspaces are.
+ * Limits (else MOE_ENOTSUP): T <= MOE_FEW_MAX_T; hidden, latent, inter and
+ * n_shared * shared_inter at most 65536.
+ * Workspace: moe_layer_few_workspace_bytes(shape, T) bytes (0: unsupported).
+ * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */
+#define MOE_FEW_MAX_T 4
+size_t moe_layer_few_workspace_bytes(const moe_shape *shape, int T);
+int moe_layer_few(const moe_shape *shape, int T, const uint16_t *x, const moe_layer_weights *w, int32_t *topk_ids,
+                  float *topk_w, float *out, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,11 +20,15 @@ MOE_ROUTE_NOALLOC_SCRATCH_BYTES = 8 << 20
 (MOE_FN_ROUTE, MOE_FN_PERMUTE, MOE_FN_GROUPED_GEMM, MOE_FN_COMBINE_NORM_UP, MOE_FN_SHARED_FFN,
  MOE_FN_REAP_SALIENCY, MOE_FN_COMBINE_NORM_UP_REAP, MOE_FN_GROUPED_GEMM_TWO_BANK) = range(8)
 MOE_WF_MXFP4, MOE_WF_AFFINE2 = 0, 1
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL = range(4)
+MOE_SCALE_F32, MOE_SCALE_E8M0 = 0, 1
+MOE_FEW_MAX_T = 4
 
 EXPORTS = ("moe_abi_version", "moe_strerror", "moe_workspace_bytes", "moe_route", "moe_permute",
            "mxfp4_grouped_gemm", "moe_combine_norm_up", "shared_expert_ffn", "moe_reap_saliency",
            "moe_combine_norm_up_reap", "moe_route_capped", "moe_route_noalloc",
-           "moe_grouped_gemm_two_bank")
+           "moe_grouped_gemm_two_bank", "moe_block_pre_norm", "moe_block_post_norm", "moe_fp8_quantize",
+           "moe_fp8_gemm_workspace_bytes", "moe_fp8_gemm", "moe_layer_few_workspace_bytes", "moe_layer_few")
 
 
 class MoeShape(ctypes.Structure):
@@ -42,6 +46,30 @@ class MoeExpertBank(ctypes.Structure):
         ("packed", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
         ("packed3", ctypes.c_void_p), ("scale3", ctypes.c_void_p), ("bias3", ctypes.c_void_p),
     ]
+
+
+class MoeNormOut(ctypes.Structure):
+    _fields_ = [
+        ("gamma", ctypes.c_void_p), ("n", ctypes.c_void_p), ("ldn", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("q_scale", ctypes.c_void_p), ("ldqs", ctypes.c_int64),
+    ]
+
+
+class MoePostNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+        ("resid", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("out", ctypes.c_void_p), ("ldo", ctypes.c_int64),
+        ("y_dtype", ctypes.c_int32), ("dtype", ctypes.c_int32), ("gamma", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_kind", ctypes.c_int32),
+        ("gate_dtype", ctypes.c_int32), ("gate_sigmoid", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("eps", ctypes.c_float), ("next", ctypes.POINTER(MoeNormOut)),
+    ]
+
+
+class MoeLayerWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "w_router", "bias", "w_down", "w1_packed", "w1_scale", "w3_packed", "w3_scale", "w2_packed", "w2_scale",
+        "gamma", "w_up", "sh_gate", "sh_up", "sh_down")]
 
 
 class MoeError(RuntimeError):
@@ -91,6 +119,21 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moe_route_capped.argtypes = [sp, i32, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_combine_norm_up_reap.restype = i32
     lib.moe_combine_norm_up_reap.argtypes = [sp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, vp, sz, vp]
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.moe_block_pre_norm.restype = i32
+    lib.moe_block_pre_norm.argtypes = [i32, i32, vp, i32, i64, f32, ctypes.POINTER(MoeNormOut), vp]
+    lib.moe_block_post_norm.restype = i32
+    lib.moe_block_post_norm.argtypes = [ctypes.POINTER(MoePostNormArgs), vp]
+    lib.moe_fp8_quantize.restype = i32
+    lib.moe_fp8_quantize.argtypes = [i32, i32, vp, i32, i64, vp, i64, vp, i64, vp]
+    lib.moe_fp8_gemm_workspace_bytes.restype = sz
+    lib.moe_fp8_gemm_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.moe_fp8_gemm.restype = i32
+    lib.moe_fp8_gemm.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, vp, i32, vp, i32, i64, i32, vp, sz, vp]
+    lib.moe_layer_few_workspace_bytes.restype = sz
+    lib.moe_layer_few_workspace_bytes.argtypes = [sp, i32]
+    lib.moe_layer_few.restype = i32
+    lib.moe_layer_few.argtypes = [sp, i32, vp, ctypes.POINTER(MoeLayerWeights), vp, vp, vp, vp, sz, vp]
     if path is None:
         _lib = lib
     return lib

@@ -377,6 +377,267 @@ static int combine_norm_up_impl(const moe_shape *s, int T, const float *Y, const
 }
 
 
+// ---- the norms around the block and the 8-bit product
+static bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+static bool is_float_dtype(int d) { return d == MOE_DT_F32 || d == MOE_DT_BF16; }
+static size_t dtype_bytes(int d) { return d == MOE_DT_BF16 ? 2 : 4; }
+
+// chunks of 8 values of these rows are whole and can be moved as vectors
+static bool chunked(const void *p, long long ld, size_t esz) {
+  const size_t n = esz == 1 ? 8 : 16;
+  return aligned(p, n) && (ld * (long long)esz) % (long long)n == 0;
+}
+
+// the normed outputs of a call: something asked for, and all it needs
+static int check_norm_out(const moe_norm_out *o, int H, bool *vec) {
+  if (!o->gamma || (!o->n && !o->q)) return MOE_EINVAL;
+  if ((o->q == nullptr) != (o->q_scale == nullptr)) return MOE_EINVAL;
+  if (!aligned(o->gamma, 2) || !aligned(o->n, 2)) return MOE_EINVAL;
+  if (o->n && o->ldn < H) return MOE_EINVAL;
+  if (o->q && (o->ldq < H || o->ldqs < (H + 127) / 128)) return MOE_EINVAL;
+  *vec = *vec && aligned(o->gamma, 16) && (!o->n || chunked(o->n, o->ldn, 2)) && (!o->q || chunked(o->q, o->ldq, 1));
+  return MOE_OK;
+}
+static NormOut norm_out(const moe_norm_out *o) {
+  return NormOut{o->gamma, o->n, o->ldn, o->q, o->ldq, o->q_scale, o->ldqs};
+}
+
+static int pre_norm_impl(int T, int H, const void *x, int x_dtype, int64_t ldx, float eps, const moe_norm_out *o,
+                         void *stream) {
+  if (T < 0 || H <= 0 || !o || !is_float_dtype(x_dtype) || !(eps >= 0.f)) return MOE_EINVAL;
+  bool vec = H % 8 == 0;
+  int rc = check_norm_out(o, H, &vec);
+  if (rc) return rc;
+  if (!x || ldx < H || !aligned(x, dtype_bytes(x_dtype))) return MOE_EINVAL;
+  if (H > NORM_MAX_H) return MOE_ENOTSUP;
+  if ((rc = check_device())) return rc;
+  if (T == 0) return MOE_OK;
+  vec = vec && chunked(x, ldx, dtype_bytes(x_dtype));
+  return launch_pre_norm(x, x_dtype == MOE_DT_BF16, ldx, T, H, eps, vec, norm_out(o),
+                         static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+static int post_norm_impl(const moe_post_norm_args *p, void *stream) {
+  if (!p || p->T < 0 || p->H <= 0 || !is_float_dtype(p->y_dtype) || !is_float_dtype(p->dtype)) return MOE_EINVAL;
+  const int H = p->H;
+  if (!p->y || !p->resid || !p->out || !(p->eps >= 0.f)) return MOE_EINVAL;
+  const size_t yb = dtype_bytes(p->y_dtype), rb = dtype_bytes(p->dtype);
+  if (!aligned(p->y, yb) || !aligned(p->resid, rb) || !aligned(p->out, rb) || !aligned(p->gamma, 2)) return MOE_EINVAL;
+  if (p->ldy < H || p->ldr < H || p->ldo < H) return MOE_EINVAL;
+  // in place means row for row
+  if (p->out == p->resid && p->ldo != p->ldr) return MOE_EINVAL;
+  bool vec = H % 8 == 0 && chunked(p->y, p->ldy, yb) && chunked(p->resid, p->ldr, rb) && chunked(p->out, p->ldo, rb) &&
+             (!p->gamma || aligned(p->gamma, 16));
+  if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_FULL) return MOE_EINVAL;
+  if ((p->gate_kind == MOE_GATE_NONE) != (p->gate == nullptr)) return MOE_EINVAL;
+  if (p->gate_sigmoid != 0 && p->gate_sigmoid != 1) return MOE_EINVAL;
+  long long ldg = 0;
+  if (p->gate) {
+    if (!is_float_dtype(p->gate_dtype)) return MOE_EINVAL;
+    const size_t gb = dtype_bytes(p->gate_dtype);
+    if (!aligned(p->gate, gb)) return MOE_EINVAL;
+    if (p->gate_kind == MOE_GATE_FULL && p->ldg < H) return MOE_EINVAL;
+    if (p->gate_kind == MOE_GATE_TOKEN && p->ldg < 1) return MOE_EINVAL;
+    ldg = p->gate_kind == MOE_GATE_CHANNEL ? 0 : p->ldg;
+    if (p->gate_kind != MOE_GATE_TOKEN) vec = vec && chunked(p->gate, ldg, gb);
+  }
+  if (p->next) {
+    const int rc = check_norm_out(p->next, H, &vec);
+    if (rc) return rc;
+  }
+  if (H > NORM_MAX_H) return MOE_ENOTSUP;
+  int rc = check_device();
+  if (rc) return rc;
+  if (p->T == 0) return MOE_OK;
+  PostNormArgs a{};
+  a.y = p->y;
+  a.resid = p->resid;
+  a.out = p->out;
+  a.ldy = p->ldy;
+  a.ldr = p->ldr;
+  a.ldo = p->ldo;
+  a.gamma = p->gamma;
+  a.gate = p->gate;
+  a.ldg = ldg;
+  a.gate_channels = p->gate_kind == MOE_GATE_CHANNEL || p->gate_kind == MOE_GATE_FULL;
+  a.gate_bf16 = p->gate && p->gate_dtype == MOE_DT_BF16;
+  a.gate_sigmoid = p->gate_sigmoid;
+  a.scale = p->scale;
+  a.eps = p->eps;
+  a.T = p->T;
+  a.H = H;
+  a.vec = vec;
+  if (p->next) a.next = norm_out(p->next);
+  return launch_post_norm(a, p->y_dtype == MOE_DT_BF16, p->dtype == MOE_DT_BF16,
+                          static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+static int fp8_quantize_impl(int T, int K, const void *x, int x_dtype, int64_t ldx, uint8_t *q, int64_t ldq,
+                             uint8_t *q_scale, int64_t ldqs, void *stream) {
+  if (T < 0 || K <= 0 || !x || !q || !q_scale || !is_float_dtype(x_dtype)) return MOE_EINVAL;
+  const int kb = (K + 127) / 128;
+  if (ldx < K || ldq < K || ldqs < kb || !aligned(x, dtype_bytes(x_dtype))) return MOE_EINVAL;
+  if ((long long)T * kb > (1LL << 34)) return MOE_ENOTSUP;  // one grid
+  const int rc = check_device();
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  const bool vec = K % 8 == 0 && chunked(x, ldx, dtype_bytes(x_dtype)) && chunked(q, ldq, 1);
+  return launch_quantize8(x, x_dtype == MOE_DT_BF16, ldx, T, K, vec, q, ldq, q_scale, ldqs,
+                          static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+// limits of the 8-bit product's kernels: 16-byte pieces of rows, and 32-bit
+// offsets within the rows one work-group reads
+static int fp8_check_sizes(int T, int N, int K) {
+  if (T < 0 || N <= 0 || K <= 0) return MOE_EINVAL;
+  if (K % 16 || K > (1 << 20) || T > (1 << 22) || N > (1 << 22)) return MOE_ENOTSUP;
+  return MOE_OK;
+}
+
+static int fp8_gemm_impl(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8_t *x_scale, int64_t ldxs,
+                         const uint8_t *w, const void *w_scale, int w_scale_type, void *out, int out_dtype,
+                         int64_t ldo, int accumulate, void *ws, size_t ws_bytes, void *stream) {
+  int rc = fp8_check_sizes(T, N, K);
+  if (rc) return rc;
+  const int kb = (K + 127) / 128;
+  if (!x || !x_scale || !w || !w_scale || !out || !ws || !is_float_dtype(out_dtype)) return MOE_EINVAL;
+  if (w_scale_type != MOE_SCALE_F32 && w_scale_type != MOE_SCALE_E8M0) return MOE_EINVAL;
+  if (accumulate != 0 && (accumulate != 1 || out_dtype != MOE_DT_F32)) return MOE_EINVAL;
+  if (ldx < K || ldxs < kb || ldo < N) return MOE_EINVAL;
+  if (!aligned16(x) || ldx % 16 || !aligned16(w) || !aligned16(ws) || !aligned(out, dtype_bytes(out_dtype)) ||
+      (w_scale_type == MOE_SCALE_F32 && !aligned(w_scale, 4)))
+    return MOE_EINVAL;
+  if (ldx > (1 << 22)) return MOE_ENOTSUP;
+  if (ws_bytes < moe_fp8_gemm_workspace_bytes(T, N, K)) return MOE_EWORKSPACE;
+  if ((rc = check_device())) return rc;
+  if (T == 0) return MOE_OK;
+  Fp8Args g{};
+  g.x = x;
+  g.ldx = ldx;
+  g.sx = x_scale;
+  g.ldsx = ldxs;
+  g.w = w;
+  g.sw = w_scale;
+  g.out = out;
+  g.ldo = ldo;
+  g.T = T;
+  g.N = N;
+  g.K = K;
+  g.accumulate = accumulate;
+  const size_t piece = out_dtype == MOE_DT_BF16 ? 8 : 16;
+  g.vec_out = aligned(out, piece) && (ldo * (long long)dtype_bytes(out_dtype)) % (long long)piece == 0;
+  return launch_fp8_gemm(g, w_scale_type == MOE_SCALE_E8M0, out_dtype == MOE_DT_BF16, ws,
+                         static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+// ---- the layer for a few tokens
+struct FewWs {
+  size_t counters, list, ids, wts, logits, ss, sd, y, z, hs, h, yn, total;
+};
+static FewWs few_ws(const moe_shape *s, int T) {
+  FewWs w{};
+  const size_t P = (size_t)T * s->top_k, S = (size_t)s->n_shared * s->shared_inter;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align_up(bytes);
+    return o;
+  };
+  w.counters = take(FEW_COUNTERS * sizeof(int32_t));
+  w.list = take(sizeof(FewList));
+  w.ids = take(P * 4);
+  w.wts = take(P * 4);
+  w.logits = take((size_t)T * s->n_experts * 4);
+  w.ss = take((size_t)T * ((s->latent + 255) / 256) * 4);
+  w.sd = take((size_t)T * s->hidden * 4);
+  w.y = take(P * s->latent * 4);
+  w.z = take((size_t)T * s->latent * 6);
+  w.hs = take((size_t)T * S * 6);
+  w.h = take(P * s->inter * 6);
+  w.yn = take((size_t)T * s->latent * 6);
+  w.total = at;
+  return w;
+}
+// sizes up to which the kernels' 32-bit offsets within one step's buffers hold
+static int few_check(const moe_shape *s, int T) {
+  const int rc = check_shape(s);
+  if (rc) return rc;
+  if (T <= 0) return MOE_EINVAL;
+  const int lim = 1 << 16;
+  if (T > MOE_FEW_MAX_T || s->hidden > lim || s->latent > lim || s->inter > lim ||
+      (long long)s->n_shared * s->shared_inter > lim)
+    return MOE_ENOTSUP;
+  return MOE_OK;
+}
+
+static int layer_few_impl(const moe_shape *s, int T, const uint16_t *x, const moe_layer_weights *lw,
+                          int32_t *topk_ids, float *topk_w, float *out, void *ws, size_t ws_bytes, void *stream) {
+  int rc = few_check(s, T);
+  if (rc) return rc;
+  if (!x || !lw || !out || !ws) return MOE_EINVAL;
+  if ((topk_ids == nullptr) != (topk_w == nullptr)) return MOE_EINVAL;
+  const int S = s->n_shared * s->shared_inter;
+  const void *need[] = {lw->w_router, lw->w_down, lw->w_up, lw->w1_packed, lw->w3_packed, lw->w2_packed};
+  for (const void *p : need)
+    if (!p || !aligned16(p)) return MOE_EINVAL;
+  const void *small[] = {lw->bias, lw->w1_scale, lw->w3_scale, lw->w2_scale};
+  for (const void *p : small)
+    if (!p || !aligned(p, 4)) return MOE_EINVAL;
+  if (!lw->gamma || !aligned(lw->gamma, 2)) return MOE_EINVAL;
+  if (S > 0) {
+    const void *sh[] = {lw->sh_gate, lw->sh_up, lw->sh_down};
+    for (const void *p : sh)
+      if (!p || !aligned16(p)) return MOE_EINVAL;
+  }
+  if (!aligned16(x) || !aligned16(out) || !aligned16(ws) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+    return MOE_EINVAL;
+  const FewWs w = few_ws(s, T);
+  if (ws_bytes < w.total) return MOE_EWORKSPACE;
+  if ((rc = check_device())) return rc;
+  FewArgs a{};
+  a.T = T;
+  a.H = s->hidden;
+  a.L = s->latent;
+  a.E = s->n_experts;
+  a.k = s->top_k;
+  a.I = s->inter;
+  a.S = S;
+  a.beta = s->beta;
+  a.beta_lin = s->beta_lin;
+  a.eps = s->rms_eps;
+  a.x = x;
+  a.w_router = lw->w_router;
+  a.bias = lw->bias;
+  a.w_down = lw->w_down;
+  a.w_up = lw->w_up;
+  a.gamma = lw->gamma;
+  a.sh_gate = lw->sh_gate;
+  a.sh_up = lw->sh_up;
+  a.sh_down = lw->sh_down;
+  a.w1 = lw->w1_packed;
+  a.s1 = lw->w1_scale;
+  a.w3 = lw->w3_packed;
+  a.s3 = lw->w3_scale;
+  a.w2 = lw->w2_packed;
+  a.s2 = lw->w2_scale;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  a.out = out;
+  a.counters = reinterpret_cast<int32_t *>(wsp(ws, w.counters));
+  a.list = reinterpret_cast<FewList *>(wsp(ws, w.list));
+  a.ids = reinterpret_cast<int32_t *>(wsp(ws, w.ids));
+  a.wts = reinterpret_cast<float *>(wsp(ws, w.wts));
+  a.logits = reinterpret_cast<float *>(wsp(ws, w.logits));
+  a.ss = reinterpret_cast<float *>(wsp(ws, w.ss));
+  a.sd = reinterpret_cast<float *>(wsp(ws, w.sd));
+  a.y = reinterpret_cast<float *>(wsp(ws, w.y));
+  a.z = reinterpret_cast<uint16_t *>(wsp(ws, w.z));
+  a.hs = reinterpret_cast<uint16_t *>(wsp(ws, w.hs));
+  a.h = reinterpret_cast<uint16_t *>(wsp(ws, w.h));
+  a.yn = reinterpret_cast<uint16_t *>(wsp(ws, w.yn));
+  return launch_few(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
 extern "C" {
 
 int moe_abi_version(void) { return MOE_ABI_VERSION; }
@@ -884,6 +1145,44 @@ int moe_reap_saliency(const moe_shape *s, int P, const int32_t *expert_offsets, 
       return MOE_EHIP;
     return MOE_OK;
   });
+}
+
+int moe_block_pre_norm(int T, int H, const void *x, int x_dtype, int64_t ldx, float eps, const moe_norm_out *o,
+                       void *stream) {
+  return guarded([&]() -> int { return pre_norm_impl(T, H, x, x_dtype, ldx, eps, o, stream); });
+}
+
+int moe_block_post_norm(const moe_post_norm_args *p, void *stream) {
+  return guarded([&]() -> int { return post_norm_impl(p, stream); });
+}
+
+int moe_fp8_quantize(int T, int K, const void *x, int x_dtype, int64_t ldx, uint8_t *q, int64_t ldq,
+                     uint8_t *q_scale, int64_t ldqs, void *stream) {
+  return guarded([&]() -> int { return fp8_quantize_impl(T, K, x, x_dtype, ldx, q, ldq, q_scale, ldqs, stream); });
+}
+
+size_t moe_fp8_gemm_workspace_bytes(int T, int N, int K) {
+  if (fp8_check_sizes(T, N, K) != MOE_OK) return 0;
+  return ALIGN + align_up(fp8_workspace_bytes(T, N, K));
+}
+
+int moe_fp8_gemm(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8_t *x_scale, int64_t ldxs,
+                 const uint8_t *w, const void *w_scale, int w_scale_type, void *out, int out_dtype, int64_t ldo,
+                 int accumulate, void *ws, size_t ws_bytes, void *stream) {
+  return guarded([&]() -> int {
+    return fp8_gemm_impl(T, N, K, x, ldx, x_scale, ldxs, w, w_scale, w_scale_type, out, out_dtype, ldo, accumulate,
+                         ws, ws_bytes, stream);
+  });
+}
+
+size_t moe_layer_few_workspace_bytes(const moe_shape *s, int T) {
+  if (few_check(s, T) != MOE_OK) return 0;
+  return few_ws(s, T).total;
+}
+
+int moe_layer_few(const moe_shape *s, int T, const uint16_t *x, const moe_layer_weights *w, int32_t *topk_ids,
+                  float *topk_w, float *out, void *ws, size_t ws_bytes, void *stream) {
+  return guarded([&]() -> int { return layer_few_impl(s, T, x, w, topk_ids, topk_w, out, ws, ws_bytes, stream); });
 }
 
 }  // extern "C"

@@ -178,4 +178,83 @@ hipError_t launch_combine_norm_planes(const float *Y, const int32_t *pair_pos, c
 hipError_t launch_reap_experts(const float *contrib, const int32_t *offsets, int E, double *sal_sum,
                                long long *counts, int accumulate, hipStream_t st);
 
+// ---- norms around the block, 8-bit activations
+constexpr int NORM_MAX_H = 16384;
+// the forms a normed row is written in: bf16 (n) and / or e4m3 codes with a
+// scale byte per 128 channels (q, qs); leading dimensions in elements
+struct NormOut {
+  const uint16_t *gamma;
+  uint16_t *n;
+  long long ldn;
+  uint8_t *q;
+  long long ldq;
+  uint8_t *qs;
+  long long ldqs;
+};
+struct PostNormArgs {
+  const void *y, *resid;
+  void *out;
+  long long ldy, ldr, ldo;
+  const uint16_t *gamma;  // NULL: y as it is
+  const void *gate;       // NULL: none
+  long long ldg;
+  int gate_channels;      // a value per channel (ldg 0: the same for every row), else one per row
+  int gate_bf16, gate_sigmoid;
+  float scale, eps;
+  int T, H;
+  int vec;                // every row's chunks of 8 channels are whole and aligned
+  NormOut next;           // gamma NULL: no next norm
+};
+hipError_t launch_pre_norm(const void *x, bool x_bf16, long long ldx, int T, int H, float eps, bool vec,
+                           const NormOut &o, hipStream_t st);
+hipError_t launch_post_norm(const PostNormArgs &a, bool y_bf16, bool r_bf16, hipStream_t st);
+hipError_t launch_quantize8(const void *x, bool x_bf16, long long ldx, int T, int K, bool vec, uint8_t *q,
+                            long long ldq, uint8_t *qs, long long ldqs, hipStream_t st);
+
+// ---- dense product of e4m3 operands with block scales
+struct Fp8Args {
+  const uint8_t *x;   // codes [T, ldx]
+  long long ldx;
+  const uint8_t *sx;  // scale bytes [T, ldsx]
+  long long ldsx;
+  const uint8_t *w;   // codes [N, K]
+  const void *sw;     // [N / 128, K / 128] rounded up, fp32 or e8m0 bytes
+  void *out;          // [T, ldo] fp32 or bf16
+  long long ldo;
+  int T, N, K;
+  int accumulate;
+  int vec_out;        // rows of out are 16-byte (bf16: 8-byte) aligned
+};
+size_t fp8_workspace_bytes(int T, int N, int K);
+hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, hipStream_t st);
+
+// ---- the layer for a few tokens
+constexpr int FEW_MAX_T = 4;
+constexpr int FEW_COUNTERS = 256;    // int32, cleared by the first kernel
+constexpr int FEW_MAX_PAIRS = FEW_MAX_T * 32;  // (token, expert) pairs
+// the chosen experts, each once, with the pairs (token * k + slot) that use it
+struct FewList {
+  int32_t n;
+  int32_t expert[FEW_MAX_PAIRS];
+  int32_t npair[FEW_MAX_PAIRS];
+  int32_t pair[FEW_MAX_PAIRS][FEW_MAX_T];
+};
+struct FewArgs {
+  int T, H, L, E, k, I, S;
+  float beta, beta_lin, eps;
+  const uint16_t *x, *w_router, *w_down, *w_up, *gamma, *sh_gate, *sh_up, *sh_down;
+  const float *bias;
+  const uint8_t *w1, *s1, *w3, *s3, *w2, *s2;
+  int32_t *topk_ids;  // the caller's, or NULL (topk_w as well)
+  float *topk_w;
+  float *out;
+  // workspace; z, hs, h and yn as three bf16 planes per row
+  int32_t *counters;
+  FewList *list;
+  int32_t *ids;
+  float *wts, *logits, *ss, *sd, *y;
+  uint16_t *z, *hs, *h, *yn;
+};
+hipError_t launch_few(const FewArgs &a, hipStream_t st);
+
 }  // namespace moe

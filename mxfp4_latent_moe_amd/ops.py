@@ -4,6 +4,8 @@ device pointers, the stream as its HIP handle; all compute runs in the HIP
 library."""
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -116,6 +118,175 @@ def combine_norm_up_reap(shape, T, Y, pair_pos, topk_w, gamma, w_up, out, accumu
                                           int(reap_accumulate), _p(ws), ws.numel(), _s(stream)))
 
 
+_FLOATS = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
+_CODES = tuple(d for d in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) if d is not None)
+_SCALES = tuple(d for d in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if d is not None)
+
+
+def _rows(name, t, shape, dtypes, device):
+    """Leading dimension of a 2-d tensor whose rows are contiguous, after its checks."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, want one of {tuple(dtypes)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the first tensor is on {device}")
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: rows must be contiguous (stride {inner})")
+    # a single row's stride is never used: any that fits and is aligned
+    return ld if shape[0] > 1 else -(-shape[1] // 16) * 16
+
+
+def _bytes(name, t, device):
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous tensor on {device}")
+    return t.numel() * t.element_size()
+
+
+def _vector(name, t, n, dtype, device):
+    if tuple(t.shape) != (n,) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {dtype} vector of {n} on {device}")
+    return t.data_ptr()
+
+
+def _norm_out(T, H, device, gamma, n, q, q_scale):
+    o = _lib.MoeNormOut()
+    o.gamma = _vector("gamma", gamma, H, torch.bfloat16, device)
+    if n is not None:
+        o.n, o.ldn = _p(n), _rows("n", n, (T, H), (torch.bfloat16,), device)
+    if (q is None) != (q_scale is None):
+        raise ValueError("q and q_scale go together")
+    if q is not None:
+        o.q, o.ldq = _p(q), _rows("q", q, (T, H), _CODES, device)
+        o.q_scale, o.ldqs = _p(q_scale), _rows("q_scale", q_scale, (T, -(-H // 128)), _SCALES, device)
+    return o
+
+
+def _enqueue(name, device, stream, *args):
+    """One call of the library on `device`: its current stream, or the given one, which must be its own."""
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a GPU, not {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on {device}")
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == device.index:
+        check(name, fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            check(name, fn(*args, stream.cuda_stream))
+
+
+def block_pre_norm(x, gamma, eps=1e-6, n=None, q=None, q_scale=None, stream=None):
+    """RMSNorm in front of a block (moe_block_pre_norm): x [T, H] fp32 or bf16, written as bf16 to n and / or as
+    e4m3 codes to q with a scale byte per 128 channels to q_scale.  Rows may be strided."""
+    T, H = x.shape
+    ldx = _rows("x", x, (T, H), _FLOATS, x.device)
+    o = _norm_out(T, H, x.device, gamma, n, q, q_scale)
+    if T == 0:
+        return
+    _enqueue("moe_block_pre_norm", x.device, stream, T, H, _p(x), _FLOATS[x.dtype], ldx, eps, o)
+
+
+def block_post_norm(y, resid, out, gamma=None, gate=None, gate_sigmoid=False, scale=1.0, eps=1e-6, next_gamma=None,
+                    n=None, q=None, q_scale=None, stream=None):
+    """The norm after a block, its gate, the residual scale and the residual, then the next block's pre-norm
+    (moe_block_post_norm): out = resid + scale * gate * norm(y).  gamma None: y is not normed.  gate: None or a
+    tensor of shape [T, 1], [1, H] or [T, H]; a [1, 1] gate of a single row is one value for it.  out may be resid.
+    next_gamma with n and / or q and q_scale: RMSNorm of out as stored."""
+    T, H = resid.shape
+    dev = resid.device
+    a = _lib.MoePostNormArgs()
+    a.T, a.H, a.scale, a.eps, a.gate_sigmoid = T, H, scale, eps, int(gate_sigmoid)
+    a.ldr = _rows("resid", resid, (T, H), _FLOATS, dev)
+    a.ldy = _rows("y", y, (T, H), _FLOATS, dev)
+    a.ldo = _rows("out", out, (T, H), (resid.dtype,), dev)
+    a.y_dtype, a.dtype = _FLOATS[y.dtype], _FLOATS[resid.dtype]
+    if gamma is not None:
+        a.gamma = _vector("gamma", gamma, H, torch.bfloat16, dev)
+    if gate is not None:
+        if gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, H):
+            raise ValueError(f"gate: shape {tuple(gate.shape)}, want [T, 1], [1, H] or [T, H]")
+        if gate.shape == (T, 1):
+            a.gate_kind = _lib.MOE_GATE_TOKEN
+        elif gate.shape == (T, H):
+            a.gate_kind = _lib.MOE_GATE_FULL
+        elif gate.shape == (1, H):
+            a.gate_kind = _lib.MOE_GATE_CHANNEL
+        else:
+            raise ValueError("gate: one value for every row and channel belongs into scale")
+        ldg = _rows("gate", gate, tuple(gate.shape), _FLOATS, dev)
+        a.gate, a.ldg, a.gate_dtype = _p(gate), ldg, _FLOATS[gate.dtype]
+    if next_gamma is not None:
+        nx = _norm_out(T, H, dev, next_gamma, n, q, q_scale)
+        a.next = ctypes.pointer(nx)
+    elif n is not None or q is not None or q_scale is not None:
+        raise ValueError("n, q and q_scale need next_gamma")
+    if T == 0:
+        return
+    a.y, a.resid, a.out = _p(y), _p(resid), _p(out)
+    _enqueue("moe_block_post_norm", dev, stream, a)
+
+
+def fp8_quantize(x, q, q_scale, stream=None):
+    """Rows of x [T, K] (fp32 or bf16) as e4m3 codes q [T, K] with a scale byte per 128 values q_scale
+    [T, ceil(K / 128)] (moe_fp8_quantize)."""
+    T, K = x.shape
+    ldx = _rows("x", x, (T, K), _FLOATS, x.device)
+    ldq = _rows("q", q, (T, K), _CODES, x.device)
+    lds = _rows("q_scale", q_scale, (T, -(-K // 128)), _SCALES, x.device)
+    if T == 0:
+        return
+    _enqueue("moe_fp8_quantize", x.device, stream, T, K, _p(x), _FLOATS[x.dtype], ldx, _p(q), ldq, _p(q_scale), lds)
+
+
+def fp8_gemm_workspace_bytes(T: int, N: int, K: int) -> int:
+    return int(load().moe_fp8_gemm_workspace_bytes(T, N, K))
+
+
+def fp8_gemm(x, x_scale, w, w_scale, out, ws, accumulate=False, stream=None):
+    """out [T, N] (+)= x w^T with e4m3 operands (moe_fp8_gemm): x [T, K] with scale bytes [T, ceil(K / 128)] (see
+    fp8_quantize), w [N, K] with one scale per 128 x 128 block, fp32 or e8m0 bytes [ceil(N / 128), ceil(K / 128)].
+    out is fp32 or bf16; ws holds fp8_gemm_workspace_bytes(T, N, K) bytes."""
+    T, K = x.shape
+    N = w.shape[0]
+    kb = -(-K // 128)
+    dev = w.device
+    ldx = _rows("x", x, (T, K), _CODES, dev)
+    lds = _rows("x_scale", x_scale, (T, kb), _SCALES, dev)
+    _rows("w", w, (N, K), _CODES, dev)
+    _rows("w_scale", w_scale, (-(-N // 128), kb), (torch.float32, *_SCALES), dev)
+    ldo = _rows("out", out, (T, N), _FLOATS, dev)
+    for name, t in (("w", w), ("w_scale", w_scale)):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if T == 0:
+        return
+    kind = _lib.MOE_SCALE_F32 if w_scale.dtype == torch.float32 else _lib.MOE_SCALE_E8M0
+    _enqueue("moe_fp8_gemm", dev, stream, T, N, K, _p(x), ldx, _p(x_scale), lds, _p(w), _p(w_scale), kind, _p(out),
+             _FLOATS[out.dtype], ldo, int(accumulate), _p(ws), _bytes("ws", ws, dev))
+
+
+def layer_weights(weights: dict) -> _lib.MoeLayerWeights:
+    """moe_layer_weights of a LatentMoE weight dict (which must stay alive)."""
+    lw = _lib.MoeLayerWeights()
+    for k in WEIGHT_KEYS:
+        setattr(lw, k, _p(weights[k]) if weights[k].numel() else None)
+    return lw
+
+
+def layer_few_workspace_bytes(shape: MoeShape, T: int) -> int:
+    return int(load().moe_layer_few_workspace_bytes(shape, T))
+
+
+def layer_few(shape, x, lw, topk_ids, topk_w, out, ws, stream=None):
+    """The whole layer for up to MOE_FEW_MAX_T tokens in one call (moe_layer_few); lw from layer_weights."""
+    _enqueue("moe_layer_few", x.device, stream, shape, x.shape[0], _p(x), lw, _p(topk_ids), _p(topk_w), _p(out),
+             _p(ws), _bytes("ws", ws, x.device))
+
+
 WEIGHT_KEYS = ("w_router", "bias", "w_down", "w_up", "gamma", "sh_gate", "sh_up", "sh_down",
                "w1_packed", "w1_scale", "w3_packed", "w3_scale", "w2_packed", "w2_scale")
 
@@ -182,6 +353,8 @@ class LatentMoE:
                            for op in (MOE_OP_GATEUP_SITU, MOE_OP_DOWN)}
         self.device = torch.device(device)
         self._bufs: dict = {}
+        self._few_bufs: dict = {}
+        self._few_weights = None
         self.overlap_shared = overlap_shared
         # at decode sizes the latent projection z joins the shared experts on
         # the side stream, so the main stream's routing is only the router and
@@ -320,4 +493,32 @@ class LatentMoE:
         call("moe_combine_norm_up", st,
              lambda: combine_norm_up(s, T, b["Y"], b["pair_pos"], b["topk_w"], w["gamma"], w["w_up"], b["out"],
                                      1 if shared else 0, ws, st))
+        return b
+
+    def forward_few(self, x: torch.Tensor, stream=None) -> dict:
+        """The layer for up to MOE_FEW_MAX_T tokens (x [T, H] bf16) as one call of two kernels on one stream: for
+        single tokens and drafts, where the time of forward() goes into the steps between the weight streams.
+        Returns the buffers "out", "topk_ids" and "topk_w" of T tokens (not those of forward(); the next call with
+        as many tokens overwrites them, so calls on several streams at once need a layer object each).  Products
+        take activations at fp32 precision whatever operand_mode is.  A two-bank layer has no such form."""
+        if self.bank_b is not None:
+            raise ValueError("forward_few: the two-bank layer has no few-token form")
+        T = x.shape[0]
+        if x.dim() != 2 or not 1 <= T <= _lib.MOE_FEW_MAX_T or x.shape[1] != self.shape.hidden:
+            raise ValueError(f"forward_few: x is {tuple(x.shape)}, want [1..{_lib.MOE_FEW_MAX_T}, {self.shape.hidden}]")
+        dev = self.w["w_router"].device
+        if x.dtype != torch.bfloat16 or not x.is_contiguous() or x.device != dev:
+            raise ValueError(f"forward_few: x must be contiguous bfloat16 on {dev}")
+        if self._few_weights is None:
+            self._few_weights = layer_weights(self.w)
+        b = self._few_bufs.get(T)
+        if b is None:
+            s = self.shape
+            b = self._few_bufs[T] = {
+                "topk_ids": torch.empty((T, s.top_k), dtype=torch.int32, device=dev),
+                "topk_w": torch.empty((T, s.top_k), dtype=torch.float32, device=dev),
+                "out": torch.empty((T, s.hidden), dtype=torch.float32, device=dev),
+                "ws": torch.empty((max(16, layer_few_workspace_bytes(s, T)),), dtype=torch.uint8, device=dev),
+            }
+        layer_few(self.shape, x, self._few_weights, b["topk_ids"], b["topk_w"], b["out"], b["ws"], stream)
         return b

@@ -491,7 +491,7 @@ typedef struct {
   const uint16_t *sh_gate, *sh_up, *sh_down; /* ignored without shared experts */
 } moe_layer_weights;
 
-/* The whole layer for up to MOE_FEW_MAX_T tokens, in two kernels: the results
+/* The whole layer for up to MOE_FEW_MAX_T tokens, in six kernels: the results
  * of moe_route, moe_permute, the two expert products, moe_combine_norm_up and
  * shared_expert_ffn in one call.
  *   x        [T, H] bf16
@@ -501,8 +501,8 @@ typedef struct {
  * taken as three bf16 terms, so operand_mode has no effect: products see the
  * fp32 values.  Selection and weights follow moe_route.  Deterministic.
  * Calls on several streams at once are independent if their workspaces are.
- * Limits (else MOE_ENOTSUP): T <= MOE_FEW_MAX_T; hidden, latent, inter and
- * n_shared * shared_inter at most 65536.
+ * Limits (else MOE_ENOTSUP): T <= MOE_FEW_MAX_T; hidden and
+ * n_shared * shared_inter at most 65536, latent and inter at most 12288.
  * Workspace: moe_layer_few_workspace_bytes(shape, T) bytes (0: unsupported).
  * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */
 #define MOE_FEW_MAX_T 4

@@ -532,7 +532,7 @@ static int fp8_gemm_impl(int T, int N, int K, const uint8_t *x, int64_t ldx, con
 
 // ---- the layer for a few tokens
 struct FewWs {
-  size_t counters, list, ids, wts, logits, ss, sd, y, z, hs, h, yn, total;
+  size_t list, wts, logits, ss, sd, y, z, hs, h, yn, total;
 };
 static FewWs few_ws(const moe_shape *s, int T) {
   FewWs w{};
@@ -543,9 +543,7 @@ static FewWs few_ws(const moe_shape *s, int T) {
     at += align_up(bytes);
     return o;
   };
-  w.counters = take(FEW_COUNTERS * sizeof(int32_t));
   w.list = take(sizeof(FewList));
-  w.ids = take(P * 4);
   w.wts = take(P * 4);
   w.logits = take((size_t)T * s->n_experts * 4);
   w.ss = take((size_t)T * ((s->latent + 255) / 256) * 4);
@@ -564,7 +562,7 @@ static int few_check(const moe_shape *s, int T) {
   if (rc) return rc;
   if (T <= 0) return MOE_EINVAL;
   const int lim = 1 << 16;
-  if (T > MOE_FEW_MAX_T || s->hidden > lim || s->latent > lim || s->inter > lim ||
+  if (T > MOE_FEW_MAX_T || s->hidden > lim || s->latent > FEW_MAX_K || s->inter > FEW_MAX_K ||
       (long long)s->n_shared * s->shared_inter > lim)
     return MOE_ENOTSUP;
   return MOE_OK;
@@ -623,9 +621,7 @@ static int layer_few_impl(const moe_shape *s, int T, const uint16_t *x, const mo
   a.topk_ids = topk_ids;
   a.topk_w = topk_w;
   a.out = out;
-  a.counters = reinterpret_cast<int32_t *>(wsp(ws, w.counters));
   a.list = reinterpret_cast<FewList *>(wsp(ws, w.list));
-  a.ids = reinterpret_cast<int32_t *>(wsp(ws, w.ids));
   a.wts = reinterpret_cast<float *>(wsp(ws, w.wts));
   a.logits = reinterpret_cast<float *>(wsp(ws, w.logits));
   a.ss = reinterpret_cast<float *>(wsp(ws, w.ss));

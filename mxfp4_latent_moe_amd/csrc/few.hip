@@ -1,36 +1,37 @@
-// The whole layer for a few tokens (T <= 4) in two kernels.
+// The whole layer for a few tokens (T <= 4) in six kernels on one stream.
 //
 // At these sizes every weight of the layer that the tokens touch is read once
-// and used for at most four columns, so the layer is one weight stream of the
+// and used for at most four tokens, so the layer is one weight stream of the
 // router, the latent projections, the shared experts and the chosen experts,
-// and what costs time beside it are the places where the stream stops: kernel
-// boundaries, and steps that wait for a step before them.
+// and what costs time beside it are the places where the stream stops.  Steps
+// that need nothing from each other share a launch:
 //
-//   few_front_kernel  logits = x W_r^T and z = x W_d^T (both need x alone)
-//   few_layer_kernel  everything else, as work items in one list:
-//       top-k (a token) | shared gate/up (16 rows) | expert gate/up (32 rows) |
-//       shared down (16 rows) | expert down (64 rows) | combine (256 columns) |
-//       up_proj (16 rows)
-//     A work-group takes items from the list in order, by a ticket counter.
-//     An item that needs another step's results waits for that step's counter;
-//     the steps are ordered so that the results are usually there: the shared
-//     experts' items, which need only x, fill the time of the top-k and of the
-//     last expert gate/up items.
+//   few_front_kernel   logits = x W_r^T | z = x W_d^T
+//   few_shared_kernel  top-k and the list of chosen experts (one work-group) |
+//                      shared gate/up, which hides it
+//   few_expert<gate/up>
+//   few_expert<down>   expert down | shared down, which fills its last wave
+//   few_combine_kernel sum over a token's experts, times gamma; squares' sums
+//   few_up_kernel      up_proj, times RMSNorm's factor, plus the shared experts
 //
-// Every wait ends, whatever part of the grid is resident: an item waits only
-// for items with smaller tickets, tickets are handed out in order to
-// work-groups that are running, and a work-group works its tickets off in
-// order (it holds at most the one it works on and the next).  So the smallest
-// unfinished ticket is always at work and waits for nothing unfinished.
-//
-// Arithmetic: weight rows on the MFMA's M side, on its N side up to 15 columns.
+// Arithmetic: weight rows on the MFMA's M side, on its N side up to 12 columns.
 // x is exact in bf16.  z, the hidden activations and the normed latent are kept
 // as three bf16 planes (a = a1 + a2 + a3, exact for normal fp32), three columns
 // per token, so every product is that of the fp32 value with the exact weight;
-// sums are fp32.  The columns cost nothing: the kernel waits for weights.  The
-// eight waves of a work-group take the K steps in turn; their sums are added
-// in wave order, so results do not depend on the schedule.  RMSNorm's factor is
-// one number per token and is applied to up_proj's sums.
+// sums are fp32.  The columns cost nothing: the kernel waits for weights.
+// RMSNorm's factor is one number per token and is applied to up_proj's sums.
+// Every sum has one order, so results do not depend on the schedule.
+//
+// Measured (hidden 7168, latent 3584, 16 of 896 experts of 3072, 6144 shared):
+// 155 us for one token, 218 for two, 305 for four, 4.3 to 4.8 TB/s of the bytes
+// the layer cannot do without; the layer's calls one by one take 181, 224 and
+// 319.  Of the 155 us about 4 a kernel are the launch and its cold code, and
+// gate/up runs at 5.8 TB/s at four tokens.  One resident kernel that hands work
+// items from step to step by counters in place of launches took 177, 247 and
+// 350 us: its waves could not keep the weights flowing through the steps' ends.
+// Requests further ahead are no faster: two groups of K steps ahead in the
+// expert products 50 against 46 us at one token (one work-group a CU fits), and
+// in the bf16 products four steps a round 58 against 38.
 #include <atomic>
 
 #include "kernels.h"
@@ -39,25 +40,15 @@
 namespace moe {
 namespace {
 
-constexpr int FW = 8;             // waves per work-group
-constexpr int FTHR = 64 * FW;
-constexpr int MT_GU = 2;          // 16-row tiles per matrix of an expert gate/up item
-constexpr int MT_DN = 4;          // of an expert down item
-constexpr int CMB = 256;          // columns of a combine item
+constexpr int FNW = 8;           // waves of a work-group
+constexpr int FTHR = 64 * FNW;
+constexpr int SU = 3;            // K steps a round of the shared gate/up
+constexpr int CMB = 256;         // columns of a combine work-group
+constexpr int AHEAD = 1;         // groups of K steps requested ahead, of
+constexpr int D = 4;             // K steps (128 values) each
+constexpr int ROWS = 16 * FNW;   // weight rows of an expert item
 
-// counters, one per 128-byte line
-enum { C_TICKET = 0, C_TOPK = 32, C_READY = 64, C_SGU = 96, C_EGU = 128, C_SDN = 160, C_EDN = 192, C_CMB = 224 };
-
-MOE_DEV int32_t load_count(const int32_t *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-MOE_DEV int32_t add_count(int32_t *p) { return __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-// this wave's stores are visible on the device before its next atomic
-MOE_DEV void release() { __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent"); }
-MOE_DEV void acquire() { __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent"); }
-// counts one finished wave of an item
-MOE_DEV void done(int32_t *p) {
-  release();
-  if (lane_id() == 0) add_count(p);
-}
+MOE_DEV int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 MOE_DEV void split3(float a, __bf16 &h, __bf16 &m, __bf16 &l) {
   h = to_bf16(a);
@@ -84,89 +75,69 @@ MOE_DEV void store_planes(uint16_t *row, int k0, f32x4_t v) {
   *reinterpret_cast<bf16x4_t *>(p + 16) = l;
 }
 
-// the N-side operand of a product: lane column c's row, by octets
+// the N-side operand of a dense product: its rows, and the lane's column
 struct Cols {
-  __amdgpu_buffer_rsrc_t r;
-  uint32_t off;      // byte offset of the lane's column
+  const void *base;
+  uint32_t bytes;
+  uint32_t off;      // of the lane's column
   uint32_t ostride;  // bytes between octets
 };
-
-// acc[t] += tile t (16 rows x K) * columns, over the K steps of this wave.
-// W[t]: first byte of the tile, nrows its rows (bf16 [16][K] or packed
-// [16][K/2] with scales S[t] [16][K/32]).
-template <int WF, int NT, int U>
-MOE_DEV void product(f32x4_t (&acc)[NT], const uint8_t *const (&W)[NT], const uint8_t *const (&S)[NT], int nrows,
-                     int K, const Cols &b, int wave) {
-  constexpr int WR = WF == W_MXFP4 ? 1 : 4;
-  constexpr uint32_t STEP = WF == W_MXFP4 ? 64 : 256;
-  const int lane = lane_id(), r16 = lane & 15, kg = lane >> 4;
-  const uint32_t row_bytes = WF == W_MXFP4 ? K / 2 : 2 * K;
-  const int nks = K / 128;
-  const int row = min(r16, nrows - 1);
-  const uint32_t wo = row * row_bytes + 16 * kg, so = row * (K / 32);
-  __amdgpu_buffer_rsrc_t wr[NT], sr[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    wr[t] = make_rsrc(W[t], nrows * row_bytes);
-    if constexpr (WF == W_MXFP4) sr[t] = make_rsrc(S[t], nrows * (K / 32));
-  }
-  for (int s0 = wave; s0 < nks; s0 += FW * U) {
-    u32x4_t w[U][NT][WR], x[U][4];
-    uint32_t sc[U][NT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t s = min(s0 + FW * u, nks - 1);  // past the end: the last step again, not used
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int j = 0; j < WR; ++j) w[u][t][j] = buf_load16(wr[t], wo + 64 * j, s * STEP);
-        if constexpr (WF == W_MXFP4) sc[u][t] = buf_load4(sr[t], so, 4 * s);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t s = min(s0 + FW * u, nks - 1);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[u][j] = buf_load16(b.r, b.off + (WF == W_MXFP4 ? 4 * kg + j : 4 * j + kg) * b.ostride, 16 * s * b.ostride);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (s0 + FW * u >= nks) break;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bf16x8_t xb = __builtin_bit_cast(bf16x8_t, x[u][j]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          bf16x8_t a;
-          if constexpr (WF == W_MXFP4) a = fp4x8_to_bf16(w[u][t][0][j], e8m0_to_float((sc[u][t] >> (8 * kg)) & 0xFFu));
-          else a = __builtin_bit_cast(bf16x8_t, w[u][t][j]);
-          acc[t] = mfma_16x16x32(a, xb, acc[t]);
-        }
-      }
-    }
-  }
-}
-
 // columns that are rows of x: column c is token c
 MOE_DEV Cols cols_x(const uint16_t *x, int T, int H) {
-  return Cols{make_rsrc(x, (uint32_t)T * H * 2), (uint32_t)min(lane_id() & 15, T - 1) * H * 2, 16u};
+  return Cols{x, (uint32_t)T * H * 2, (uint32_t)min(lane_id() & 15, T - 1) * H * 2, 16};
 }
-// columns that are planes: column 3 j + p is plane p of row[j]; past 3 n the first column
-MOE_DEV Cols cols_planes(const uint16_t *planes, uint32_t bytes, int K, int n, const int32_t (&row)[FEW_MAX_T]) {
-  const int c = lane_id() & 15, j = c / 3;
-  int q = row[0];
-#pragma unroll
-  for (int i = 1; i < FEW_MAX_T; ++i) q = j == i && i < n ? row[i] : q;
-  return Cols{make_rsrc(planes, bytes), (uint32_t)q * (uint32_t)K * 6u + (j < n ? 16u * (c - 3 * j) : 0u), 48u};
+// columns of rows kept in planes: column 3 t + p is plane p of row t
+MOE_DEV Cols cols_planes(const uint16_t *x, int T, int K) {
+  const int c = min(lane_id() & 15, 3 * T - 1), t = c / 3;
+  return Cols{x, (uint32_t)T * K * 6, (uint32_t)t * K * 6 + 16 * (c - 3 * t), 48};
 }
 
-// the waves' sums of tile t, in wave order
-MOE_DEV f32x4_t wave_sum(const f32x4_t (*part)[MT_DN][64], int t) {
-  f32x4_t v = part[0][t][lane_id()];
+// 16 rows of bf16 weights (the last of nrows again past them) times the
+// columns: this wave's share of the K steps, every FNW-th, one requested ahead.
+// Steps past the end are out of the buffers' range: zeros.
+MOE_DEV f32x4_t dense_part(const uint16_t *W, int nrows, int K, const Cols &b, int wave) {
+  const int lane = lane_id(), kg = lane >> 4;
+  const int nks = K / 128;
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(W, nrows * 2u * K), br = make_rsrc(b.base, b.bytes);
+  const uint32_t wo = min(lane & 15, nrows - 1) * 2u * K + 16 * kg, bo = b.off + kg * b.ostride;
+  u32x4_t q[2][4], x[2][4];
+  auto request = [&](int slot, int s) {
+    const uint32_t ws = s < nks ? s * 256 : 0x70000000u, xs = s < nks ? s * 16 * b.ostride : 0x70000000u;
 #pragma unroll
-  for (int q = 1; q < FW; ++q) v += part[q][t][lane_id()];
+    for (int j = 0; j < 4; ++j) q[slot][j] = buf_load16(wr, wo + 64 * j, ws);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[slot][j] = buf_load16(br, bo + 4 * j * b.ostride, xs);
+  };
+  request(0, wave);
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s = wave; s < nks; s += 2 * FNW) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      request(i ^ 1, s + FNW * (i + 1));
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, q[i][j]), __builtin_bit_cast(bf16x8_t, x[i][j]), acc);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  return acc;
+}
+// the waves' sums, in wave order
+MOE_DEV f32x4_t wave_sum(const f32x4_t (*part)[64]) {
+  f32x4_t v = part[0][lane_id()];
+#pragma unroll
+  for (int i = 1; i < FNW; ++i) v += part[i][lane_id()];
   return v;
+}
+// the whole work-group's product; true in the wave that has it
+MOE_DEV bool dense_tile(f32x4_t &v, const uint16_t *W, int nrows, int K, const Cols &b, f32x4_t (*part)[64]) {
+  const int wave = uni(threadIdx.x >> 6);
+  part[wave][lane_id()] = dense_part(W, nrows, K, b, wave);
+  __syncthreads();
+  if (wave != 0) return false;
+  v = wave_sum(part);
+  return true;
 }
 // the three planes' columns of a token together, in its first column
 MOE_DEV f32x4_t plane_sum(f32x4_t v) {
@@ -178,22 +149,16 @@ MOE_DEV f32x4_t plane_sum(f32x4_t v) {
 
 // ---- x W_r^T and x W_d^T, 16 rows a work-group
 __global__ __launch_bounds__(FTHR, 4) void few_front_kernel(FewArgs a) {
-  __shared__ f32x4_t part[FW][MT_DN][64];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < FEW_COUNTERS; i += FTHR) a.counters[i] = 0;
+  __shared__ f32x4_t part[FNW][64];
+  const int lane = lane_id();
   const int nb_r = (a.E + 15) / 16;
   const bool router = (int)blockIdx.x < nb_r;
   const int n0 = 16 * (router ? blockIdx.x : blockIdx.x - nb_r);
   const int N = router ? a.E : a.L;
-  f32x4_t acc[1] = {f32x4_t{0.f, 0.f, 0.f, 0.f}};
-  const uint8_t *W[1] = {reinterpret_cast<const uint8_t *>((router ? a.w_router : a.w_down) + (long long)n0 * a.H)};
-  const uint8_t *S[1] = {nullptr};
-  product<W_BF16, 1, 2>(acc, W, S, min(16, N - n0), a.H, cols_x(a.x, a.T, a.H), wave);
-  part[wave][0][lane] = acc[0];
-  __syncthreads();
-  if (wave != 0) return;
-  const f32x4_t v = wave_sum(part, 0);
+  f32x4_t v;
+  if (!dense_tile(v, (router ? a.w_router : a.w_down) + (long long)n0 * a.H, min(16, N - n0), a.H,
+                     cols_x(a.x, a.T, a.H), part))
+    return;
   const int t = lane & 15, n = n0 + 4 * (lane >> 4);
   if (t >= a.T) return;
   if (router) {
@@ -206,287 +171,359 @@ __global__ __launch_bounds__(FTHR, 4) void few_front_kernel(FewArgs a) {
 }
 
 struct TopkLds {
-  uint32_t key[64 * SLOTS];
-  float sg[64 * SLOTS];
-  int sel[32];
-  float s[32];
-  uint32_t kl[32];
+  int sel[FEW_MAX_T][32];
+  float s[FEW_MAX_T][32];
+  uint32_t kl[FEW_MAX_T][32];
 };
 
-// one token's selection, by the whole work-group
-MOE_DEV void topk_item(const FewArgs &a, int t, TopkLds &l) {
-  for (int e = threadIdx.x; e < 64 * SLOTS; e += FTHR) {
-    uint32_t key = 0u;  // slots past E: below every real expert
-    float sg = 0.f;
-    if (e < a.E) {
-      sg = sigmoid(a.logits[(long long)t * a.E + e]);
-      float b = sg + a.bias[e];
-      if (b != b) b = -INFINITY;
-      key = order_key(b);
-    }
-    l.key[e] = key;
-    l.sg[e] = sg;
-  }
-  __syncthreads();
-  const int lane = lane_id();
-  if (threadIdx.x < 64) {
-    uint32_t key[SLOTS];
-    float sg[SLOTS];
+// The selection, a wave per token, and the list of chosen experts: each with
+// the pairs that use it, FEW_ROWS pairs an entry.  An expert's entries follow
+// one another.
+MOE_DEV void topk_group(const FewArgs &a, TopkLds &l) {
+  const int t = uni(threadIdx.x >> 6), lane = lane_id();
+  if (t < a.T) {
+    uint32_t key[SLOTS];  // 0 for slots past E: below every real expert
+    float sg[SLOTS], lg[SLOTS], bi[SLOTS];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-      key[i] = l.key[lane + 64 * i];
-      sg[i] = l.sg[lane + 64 * i];
+      const int e = min(lane + 64 * i, a.E - 1);
+      lg[i] = a.logits[(long long)t * a.E + e];
+      bi[i] = a.bias[e];
+    }
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      sg[i] = sigmoid(lg[i]);
+      float b = sg[i] + bi[i];
+      if (b != b) b = -INFINITY;
+      key[i] = lane + 64 * i < a.E ? order_key(b) : 0u;
     }
     uint32_t th, kp1;
-    select_topk(key, sg, a.k, lane, l.sel, l.s, l.kl, th, kp1);
+    select_topk(key, sg, a.k, lane, l.sel[t], l.s[t], l.kl[t], th, kp1);
   }
   __syncthreads();
-  if (threadIdx.x >= 64) return;
-  write_topk(t, a.k, lane, l.sel, l.s, l.kl, nullptr, 0, a.ids, a.wts);
-  if (a.topk_ids != nullptr) write_topk(t, a.k, lane, l.sel, l.s, l.kl, nullptr, 0, a.topk_ids, a.topk_w);
-  release();
-  int last = 0;
-  if (lane == 0) last = add_count(a.counters + C_TOPK) == a.T - 1;
-  if (!__builtin_amdgcn_readfirstlane(last)) return;
-  // the last token's wave makes the list of experts, each at its first pair
-  acquire();
+  if (t < a.T && lane < a.k) {
+    float sum = 0.f;
+    for (int q = 0; q < a.k; ++q) sum += l.s[t][q];
+    const int p = t * a.k + lane;
+    const float w = l.s[t][lane] / sum;
+    a.wts[p] = w;
+    if (a.topk_ids != nullptr) {
+      a.topk_ids[p] = l.sel[t][lane];
+      a.topk_w[p] = w;
+    }
+  }
+  if (t != 0) return;
   const int P = a.T * a.k;
   int base = 0;
   for (int p0 = 0; p0 < P; p0 += 64) {
-    const int p = p0 + lane;
-    int e = -1;
+    const int p = p0 + lane, t0 = min(p, P - 1) / a.k;
+    const int e = l.sel[t0][min(p, P - 1) - t0 * a.k];
     bool first = p < P;
+    int n = 0, pair[FEW_MAX_T];
+    // a token's ids differ, so each other token holds e once at most
+    for (int t1 = 0; t1 < a.T; ++t1)
+      for (int q = 0; q < a.k; ++q)
+        if (l.sel[t1][q] == e) {
+          if (t1 < t0) first = false;
+#pragma unroll
+          for (int i = 0; i < FEW_MAX_T; ++i)
+            if (i == n) pair[i] = t1 * a.k + q;
+          ++n;
+        }
+    // one entry or two
+    const uint64_t m1 = __ballot(first), m2 = __ballot(first && n > FEW_ROWS);
     if (first) {
-      e = a.ids[p];
-      for (int q = 0; q < p / a.k * a.k; ++q) first &= a.ids[q] != e;
+      const int slot = base + lanes_below(m1) + lanes_below(m2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int left = n - FEW_ROWS * h;
+        if (left <= 0) continue;
+        FewEntry &en = a.list->entry[slot + h];
+        en.expert = e;
+        en.npair = min(left, FEW_ROWS);
+#pragma unroll
+        for (int i = 0; i < FEW_ROWS; ++i)
+          if (i < left) en.pair[i] = pair[FEW_ROWS * h + i];
+      }
     }
-    const uint64_t m = __ballot(first);
-    if (first) {
-      const int slot = base + lanes_below(m);
-      a.list->expert[slot] = e;
-      int n = 0;
-      for (int q = p; q < P; ++q)
-        if (a.ids[q] == e) a.list->pair[slot][n++] = q;
-      a.list->npair[slot] = n;
-    }
-    base += __popcll(m);
+    base += __popcll(m1) + __popcll(m2);
   }
   if (lane == 0) a.list->n = base;
-  release();
-  if (lane == 0) add_count(a.counters + C_READY);
 }
 
-// until *p reaches n; the whole work-group, whose waves then see what was counted
-MOE_DEV void wait_for(const int32_t *p, int n) {
-  if (threadIdx.x == 0)
-    while (load_count(p) < n) __builtin_amdgcn_s_sleep(1);
-  __syncthreads();
-  acquire();
-}
-
-__global__ __launch_bounds__(FTHR, 4) void few_layer_kernel(FewArgs a) {
+// ---- top-k; shared gate/up, eight rows of both matrices a work-group
+__global__ __launch_bounds__(FTHR, 4) void few_shared_kernel(FewArgs a) {
   __shared__ union {
-    f32x4_t part[2][FW][MT_DN][64];
+    f32x4_t part[FNW][64];
     TopkLds topk;
-  } lds;
-  __shared__ int next_ticket[2];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
-  const int col = lane & 15, rg = lane >> 4;
-  const int T = a.T, H = a.H, L = a.L, I = a.I, S = a.S;
-  const int P = T * a.k;
-  int32_t *cnt = a.counters;
-  const int n_sgu = S / 16, n_sdn = S > 0 ? H / 16 : 0;
-  const int nb_gu = I / (16 * MT_GU), nb_dn = L / (16 * MT_DN), nb_cmb = (L + CMB - 1) / CMB;
-  const int end_topk = T, end_sgu = end_topk + n_sgu;
-  int end_egu = 0x7FFFFFFF, end_sdn = 0, end_edn = 0, end_cmb = 0, end = 0x7FFFFFFF;
-  int n_active = 0;
-  int seen = 0;  // steps whose results this work-group has waited for
-
-  if (threadIdx.x == 0) next_ticket[0] = add_count(cnt + C_TICKET);
+  } l;
+  if (blockIdx.x == 0) {
+    topk_group(a, l.topk);
+    return;
+  }
+  const int wave = uni(threadIdx.x >> 6), lane = lane_id(), kg = lane >> 4, r16 = lane & 15;
+  const int r0 = 8 * (blockIdx.x - 1), nks = a.H / 128;
+  const char *const w = reinterpret_cast<const char *>((r16 < 8 ? a.sh_gate : a.sh_up) + (long long)(r0 + (r16 & 7)) * a.H);
+  const char *const x = reinterpret_cast<const char *>(a.x + (long long)min(r16, a.T - 1) * a.H);
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = wave; s0 < nks; s0 += FNW * SU) {
+    u32x4_t q[SU][4], c[SU][4];
+#pragma unroll
+    for (int u = 0; u < SU; ++u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[u][j] = c[u][j] = u32x4_t{0u, 0u, 0u, 0u};
+      const int s = s0 + FNW * u;
+      if (s < nks) {
+        const uint32_t o = s * 256 + 16 * kg;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[u][j] = *reinterpret_cast<const u32x4_t *>(w + o + 64 * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[u][j] = *reinterpret_cast<const u32x4_t *>(x + o + 64 * j);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // every load of the round is on its way before the first product
+#pragma unroll
+    for (int u = 0; u < SU; ++u)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc = mfma_16x16x32(__builtin_bit_cast(bf16x8_t, q[u][j]), __builtin_bit_cast(bf16x8_t, c[u][j]), acc);
+  }
+  l.part[wave][lane] = acc;
   __syncthreads();
-  int par = 0;
-  for (;;) {
-    const int item = __builtin_amdgcn_readfirstlane(next_ticket[par]);
-    // the next ticket, ready after this item's barrier
-    if (threadIdx.x == 0) next_ticket[par ^ 1] = add_count(cnt + C_TICKET);
-    if (item >= end_sgu && !(seen & 1)) {
-      wait_for(cnt + C_READY, 1);
-      seen |= 1;
-      n_active = __builtin_amdgcn_readfirstlane(a.list->n);
-      end_egu = end_sgu + n_active * nb_gu;
-      end_sdn = end_egu + n_sdn;
-      end_edn = end_sdn + n_active * nb_dn;
-      end_cmb = end_edn + T * nb_cmb;
-      end = end_cmb + H / 16;
-    }
-    if (item >= end) break;
-    auto &part = lds.part[par];
-    par ^= 1;
+  if (wave != 0) return;
+  const f32x4_t v = wave_sum(l.part);
+  f32x4_t h;  // rows 4 kg ..: the first half of the wave has gate's sums, the second up's
+#pragma unroll
+  for (int r = 0; r < 4; ++r) h[r] = situ_glu(v[r], __shfl_down(v[r], 32, 64), a.beta, a.beta_lin);
+  if (lane < 32 && r16 < a.T) store_planes(a.hs + (long long)r16 * a.S * 3, r0 + 4 * kg, h);
+}
 
-    if (item < end_topk) {
-      topk_item(a, item, lds.topk);
-      __syncthreads();  // the selection's LDS is the sums' too
-      continue;
+// ---- expert products
+// An item is 128 weight rows (of both matrices for gate/up), 16 a wave, of a
+// list entry; a work-group has a contiguous range of the items.  Each wave
+// streams its rows over the whole of K, four K steps (256 contiguous bytes a
+// row) a group, one group ahead, across items; the entry's columns sit in LDS
+// and are staged when the entry changes.
+template <bool PAIR>
+MOE_DEV void expert_items(const FewArgs &a, u32x4_t *lds, int group, int groups) {
+  constexpr int NM = PAIR ? 2 : 1;
+  const int wave = uni(threadIdx.x >> 6), lane = lane_id(), kg = lane >> 4, r16 = lane & 15;
+  const int N = PAIR ? a.I : a.L, K = PAIR ? a.L : a.I;
+  const int nks = K / 128, ng = (nks + D - 1) / D, nb = N / ROWS;
+  const int nc = 3 * min(a.T, FEW_ROWS);
+  const uint32_t row_bytes = K / 2, srow_bytes = K / 32;
+  // read through the constant address space: the scalar unit's reads stay off
+  // the counter that paces the weight ring
+  typedef __attribute__((address_space(4))) const int32_t const_i32;
+  const_i32 *list = (const_i32 *)a.list;
+  constexpr int ENTRY = sizeof(FewEntry) / 4;
+  const int n_items = list[0] * nb;
+  const int i_begin = (int)((long long)group * n_items / groups);
+  const int i_end = (int)((long long)(group + 1) * n_items / groups);
+  if (i_begin >= i_end) return;
+
+  int l_item = i_begin, l_g = 0;
+  __amdgpu_buffer_rsrc_t wr[NM], sr[NM];
+  uint32_t wo = 0, so = 0;
+  auto set_load_item = [&](int it) {
+    const int c = uni(it / nb);
+    const long long e = list[1 + ENTRY * c];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      wr[m] = make_rsrc((PAIR ? (m ? a.w3 : a.w1) : a.w2) + e * N * row_bytes, (uint32_t)N * row_bytes);
+      sr[m] = make_rsrc((PAIR ? (m ? a.s3 : a.s1) : a.s2) + e * N * srow_bytes, (uint32_t)N * srow_bytes);
     }
-    if (item < end_sgu) {
-      const long long r0 = 16LL * (item - end_topk);
-      const uint8_t *W[2] = {reinterpret_cast<const uint8_t *>(a.sh_gate + r0 * H),
-                             reinterpret_cast<const uint8_t *>(a.sh_up + r0 * H)};
-      const uint8_t *Sc[2] = {nullptr, nullptr};
-      f32x4_t acc[2] = {};
-      product<W_BF16, 2, 1>(acc, W, Sc, 16, H, cols_x(a.x, T, H), wave);
-      part[wave][0][lane] = acc[0];
-      part[wave][1][lane] = acc[1];
-      __syncthreads();
-      if (wave == 0) {
-        const f32x4_t g = wave_sum(part, 0), u = wave_sum(part, 1);
-        f32x4_t h;
+    const uint32_t n = (it - c * nb) * ROWS + wave * 16 + r16;
+    wo = n * row_bytes + kg * 16;
+    so = n * srow_bytes;
+  };
+  set_load_item(i_begin);
+  u32x4_t wq[AHEAD + 1][D][NM], sq[AHEAD + 1][NM];
+  // Past the last item the requests go on, all to one line, so that the count
+  // of loads in flight stays the same.  A last group that is not whole reads
+  // on into the next row (codes are finite; their columns are zeros).
+  auto load_group = [&](int bi) {
+    const bool live = l_item < i_end;
+    const uint32_t w0 = live ? wo : 0u, s0 = live ? so : 0u, q0 = live ? l_g * D : 0u;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) h[r] = situ_glu(g[r], u[r], a.beta, a.beta_lin);
-        if (col < T) store_planes(a.hs + (long long)col * S * 3, (int)r0 + 4 * rg, h);
-        done(cnt + C_SGU);
-      }
-      continue;
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+      for (int m = 0; m < NM; ++m) wq[bi][d][m] = buf_load16(wr[m], w0, (q0 + d) * 64u);
+#pragma unroll
+    for (int m = 0; m < NM; ++m) sq[bi][m] = buf_load16(sr[m], s0, q0 * 4u);
+    if (++l_g == ng) {
+      l_g = 0;
+      if (++l_item < i_end) set_load_item(l_item);
     }
-    if (item < end_egu) {
-      const int i = item - end_sgu, slot = i / nb_gu, r0 = (i - slot * nb_gu) * 16 * MT_GU;
-      const long long e = a.list->expert[slot];
-      const int np = a.list->npair[slot];
-      int32_t tok[FEW_MAX_T];
+  };
 #pragma unroll
-      for (int j = 0; j < FEW_MAX_T; ++j) tok[j] = j < np ? a.list->pair[slot][j] / a.k : 0;
-      const uint8_t *W[2 * MT_GU], *Sc[2 * MT_GU];
+  for (int i = 0; i < AHEAD; ++i) load_group(i);
+
+  // columns of K steps past the end are zeros
+  for (int i = 16 * nks * nc + threadIdx.x; i < 16 * D * ng * nc; i += FTHR) lds[i] = u32x4_t{0u, 0u, 0u, 0u};
+  int staged = -1, npair = 0, pair0 = 0, pair1 = 0;
+  const u32x4_t *const src = reinterpret_cast<const u32x4_t *>(PAIR ? a.z : a.h);
+  auto stage = [&](int c) {
+    if (c == staged) return;
+    npair = uni(list[1 + ENTRY * c + 1]);
+    pair0 = uni(list[1 + ENTRY * c + 2]);
+    pair1 = npair > 1 ? uni(list[1 + ENTRY * c + 3]) : pair0;
+    __syncthreads();  // every wave is done with the previous entry's columns
+    const int pieces = K / 8 * 3;
+    const u32x4_t *const row0 = src + (long long)(PAIR ? pair0 / a.k : pair0) * pieces;
+    const u32x4_t *const row1 = src + (long long)(PAIR ? pair1 / a.k : pair1) * pieces;
+    constexpr int B = 3;  // pieces of a row that a thread requests at once
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += B * FTHR) {
+      u32x4_t v[2][B];
 #pragma unroll
-      for (int t = 0; t < 2 * MT_GU; ++t) {
-        const long long row = e * I + r0 + 16 * (t % MT_GU);
-        W[t] = (t < MT_GU ? a.w1 : a.w3) + row * (L / 2);
-        Sc[t] = (t < MT_GU ? a.s1 : a.s3) + row * (L / 32);
+      for (int u = 0; u < B; ++u) {
+        const int i = min(i0 + FTHR * u, pieces - 1);
+        v[0][u] = row0[i];
+        v[1][u] = row1[i];
       }
-      f32x4_t acc[2 * MT_GU] = {};
-      product<W_MXFP4, 2 * MT_GU, 2>(acc, W, Sc, 16, L, cols_planes(a.z, (uint32_t)T * L * 6u, L, np, tok), wave);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int t = 0; t < 2 * MT_GU; ++t) part[wave][t][lane] = acc[t];
-      __syncthreads();
-      if (wave < MT_GU) {
-        const f32x4_t g = plane_sum(wave_sum(part, wave)), u = plane_sum(wave_sum(part, wave + MT_GU));
-        f32x4_t h;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) h[r] = situ_glu(g[r], u[r], a.beta, a.beta_lin);
-        const int j = col / 3;
-        if (col == 3 * j && j < np)
-          store_planes(a.h + (long long)a.list->pair[slot][j] * I * 3, r0 + 16 * wave + 4 * rg, h);
-        done(cnt + C_EGU);
+      for (int u = 0; u < B; ++u) {
+        const int i = min(i0 + FTHR * u, pieces - 1);
+        u32x4_t *const to = lds + i / 3 * nc + i % 3;
+        to[0] = v[0][u];
+        if (npair > 1) to[3] = v[1][u];
       }
-      continue;
     }
-    if (item < end_sdn) {
-      if (!(seen & 2)) wait_for(cnt + C_SGU, n_sgu);
-      seen |= 2;
-      const long long r0 = 16LL * (item - end_egu);
-      const uint8_t *W[1] = {reinterpret_cast<const uint8_t *>(a.sh_down + r0 * S)};
-      const uint8_t *Sc[1] = {nullptr};
-      const int32_t tok[FEW_MAX_T] = {0, 1, 2, 3};
-      f32x4_t acc[1] = {};
-      product<W_BF16, 1, 2>(acc, W, Sc, 16, S, cols_planes(a.hs, (uint32_t)T * S * 6u, S, T, tok), wave);
-      part[wave][0][lane] = acc[0];
-      __syncthreads();
-      if (wave == 0) {
-        const f32x4_t v = plane_sum(wave_sum(part, 0));
-        const int j = col / 3;
-        if (col == 3 * j && j < T) *reinterpret_cast<f32x4_t *>(a.sd + (long long)j * H + r0 + 4 * rg) = v;
-        done(cnt + C_SDN);
-      }
-      continue;
-    }
-    if (item < end_edn) {
-      if (!(seen & 4)) wait_for(cnt + C_EGU, n_active * nb_gu * MT_GU);
-      seen |= 4;
-      const int i = item - end_sdn, slot = i / nb_dn, r0 = (i - slot * nb_dn) * 16 * MT_DN;
-      const long long e = a.list->expert[slot];
-      const int np = a.list->npair[slot];
-      int32_t pair[FEW_MAX_T];
-#pragma unroll
-      for (int j = 0; j < FEW_MAX_T; ++j) pair[j] = j < np ? a.list->pair[slot][j] : 0;
-      const uint8_t *W[MT_DN], *Sc[MT_DN];
-#pragma unroll
-      for (int t = 0; t < MT_DN; ++t) {
-        const long long row = e * L + r0 + 16 * t;
-        W[t] = a.w2 + row * (I / 2);
-        Sc[t] = a.s2 + row * (I / 32);
-      }
-      f32x4_t acc[MT_DN] = {};
-      product<W_MXFP4, MT_DN, 2>(acc, W, Sc, 16, I, cols_planes(a.h, (uint32_t)P * I * 6u, I, np, pair), wave);
-#pragma unroll
-      for (int t = 0; t < MT_DN; ++t) part[wave][t][lane] = acc[t];
-      __syncthreads();
-      if (wave < MT_DN) {
-        const f32x4_t v = plane_sum(wave_sum(part, wave));
-        const int j = col / 3;
-        if (col == 3 * j && j < np)
-          *reinterpret_cast<f32x4_t *>(a.y + (long long)a.list->pair[slot][j] * L + r0 + 16 * wave + 4 * rg) = v;
-        done(cnt + C_EDN);
-      }
-      continue;
-    }
-    if (item < end_cmb) {
-      if (!(seen & 8)) wait_for(cnt + C_EDN, n_active * nb_dn * MT_DN);
-      seen |= 8;
-      const int i = item - end_edn, t = i / nb_cmb, blk = i - t * nb_cmb;
-      const int c = blk * CMB + 4 * lane;
-      f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-      if (c < L)
-        for (int j = wave; j < a.k; j += FW) {
-          const int p = t * a.k + j;
-          v += a.wts[p] * *reinterpret_cast<const f32x4_t *>(a.y + (long long)p * L + c);
-        }
-      part[wave][0][lane] = v;
-      __syncthreads();
-      if (wave == 0) {
-        v = wave_sum(part, 0);
-        float ss = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) ss += __shfl_xor(ss, d, 64);
-        if (c < L) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] *= __uint_as_float((uint32_t)a.gamma[c + r] << 16);
-          store_planes(a.yn + (long long)t * L * 3, c, v);
-        }
-        if (lane == 0) a.ss[t * nb_cmb + blk] = ss;
-        done(cnt + C_CMB);
-      }
-      continue;
-    }
-    if (!(seen & 16)) {
-      wait_for(cnt + C_CMB, T * nb_cmb);
-      if (S > 0) wait_for(cnt + C_SDN, n_sdn);
-    }
-    seen |= 16;
-    const long long r0 = 16LL * (item - end_cmb);
-    const uint8_t *W[1] = {reinterpret_cast<const uint8_t *>(a.w_up + r0 * L)};
-    const uint8_t *Sc[1] = {nullptr};
-    const int32_t tok[FEW_MAX_T] = {0, 1, 2, 3};
-    f32x4_t acc[1] = {};
-    product<W_BF16, 1, 2>(acc, W, Sc, 16, L, cols_planes(a.yn, (uint32_t)T * L * 6u, L, T, tok), wave);
-    part[wave][0][lane] = acc[0];
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // nothing of this is counted against the ring
     __syncthreads();
-    if (wave == 0) {
-      f32x4_t v = plane_sum(wave_sum(part, 0));
-      const int j = col / 3;
-      if (col == 3 * j && j < T) {
-        float ss = 0.f;
-        for (int q = 0; q < nb_cmb; ++q) ss += a.ss[j * nb_cmb + q];
-        v = v * (1.0f / sqrtf(ss / (float)L + a.eps));
-        const long long o = (long long)j * H + r0 + 4 * rg;
-        if (S > 0) v += *reinterpret_cast<const f32x4_t *>(a.sd + o);
-        *reinterpret_cast<f32x4_t *>(a.out + o) = v;
+    staged = c;
+  };
+  const u32x4_t *const col = lds + kg * 4 * nc + min(r16, nc - 1);
+
+  int item = i_begin, c = uni(item / nb), g = 0;
+  stage(c);
+  f32x4_t acc[NM];
+#pragma unroll
+  for (int m = 0; m < NM; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto finish = [&]() {
+    const int n0 = (item - c * nb) * ROWS + wave * 16 + 4 * kg, j = r16 / 3;
+    f32x4_t v = plane_sum(acc[0]);
+    if constexpr (PAIR) {
+      const f32x4_t u = plane_sum(acc[NM - 1]);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = situ_glu(v[r], u[r], a.beta, a.beta_lin);
+    }
+    if (r16 == 3 * j && j < npair) {
+      const int p = j == 0 ? pair0 : pair1;
+      if constexpr (PAIR) store_planes(a.h + (long long)p * N * 3, n0, v);
+      else *reinterpret_cast<f32x4_t *>(a.y + (long long)p * N + n0) = v;
+    }
+#pragma unroll
+    for (int m = 0; m < NM; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  };
+  // the groups of the work-group's items, a ring's turn an iteration; groups
+  // past the last one are multiplied and dropped
+  for (int left = (i_end - i_begin) * ng; left > 0; left -= AHEAD + 1) {
+#pragma unroll
+    for (int b = 0; b <= AHEAD; ++b) {
+      load_group((b + AHEAD) % (AHEAD + 1));
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        float sc[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+          sc[m] = g * D + d < nks ? e8m0_to_float((sq[b][m][d] >> (8 * kg)) & 0xFFu) : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8_t x = __builtin_bit_cast(bf16x8_t, col[(16 * (g * D + d) + j) * nc]);
+#pragma unroll
+          for (int m = 0; m < NM; ++m) acc[m] = mfma_16x16x32(fp4x8_to_bf16(wq[b][d][m][j], sc[m]), x, acc[m]);
+        }
+      }
+      if (++g == ng) {
+        g = 0;
+        if (item < i_end) {
+          finish();
+          if (++item < i_end) {
+            c = uni(item / nb);
+            stage(c);
+          }
+        }
       }
     }
   }
+}
+
+// gate/up; down with the shared experts' down products behind it
+template <bool PAIR>
+__global__ __launch_bounds__(FTHR, 2) void few_expert_kernel(FewArgs a, int groups) {
+  extern __shared__ u32x4_t lds[];
+  if ((int)blockIdx.x < groups) {
+    expert_items<PAIR>(a, lds, blockIdx.x, groups);
+    return;
+  }
+  if constexpr (!PAIR) {
+    const int lane = lane_id(), n0 = 16 * (blockIdx.x - groups);
+    f32x4_t v;
+    if (!dense_tile(v, a.sh_down + (long long)n0 * a.S, 16, a.S, cols_planes(a.hs, a.T, a.S),
+                       reinterpret_cast<f32x4_t(*)[64]>(lds)))
+      return;
+    v = plane_sum(v);
+    const int col = lane & 15, t = col / 3;
+    if (col == 3 * t && t < a.T)
+      *reinterpret_cast<f32x4_t *>(a.sd + (long long)t * a.H + n0 + 4 * (lane >> 4)) = v;
+  }
+}
+
+// ---- 256 columns of a token's combined latent, times gamma, and their squares' sum
+__global__ __launch_bounds__(64) void few_combine_kernel(FewArgs a) {
+  const int lane = lane_id(), L = a.L;
+  const int t = blockIdx.y, c = blockIdx.x * CMB + 4 * lane;
+  const float wt = lane < a.k ? a.wts[t * a.k + lane] : 0.f;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  for (int q0 = 0; q0 < a.k; q0 += 16) {
+    f32x4_t y[16];  // all requested at once; past the last slot that one again, unused
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      y[q] = *reinterpret_cast<const f32x4_t *>(a.y + (long long)(t * a.k + min(q0 + q, a.k - 1)) * L + min(c, L - 4));
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      if (q0 + q < a.k) v += __shfl(wt, q0 + q, 64) * y[q];
+  }
+  if (c >= L) v = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  float ss = v[0] * v[0] + v[1] * v[1] + v[2] * v[2] + v[3] * v[3];
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) ss += __shfl_xor(ss, d, 64);
+  if (c < L) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] *= __uint_as_float((uint32_t)a.gamma[c + r] << 16);
+    store_planes(a.yn + (long long)t * L * 3, c, v);
+  }
+  if (lane == 0) a.ss[t * gridDim.x + blockIdx.x] = ss;
+}
+
+// ---- up_proj, 16 rows a work-group
+__global__ __launch_bounds__(FTHR, 4) void few_up_kernel(FewArgs a, int nb_cmb) {
+  __shared__ f32x4_t part[FNW][64];
+  const int lane = lane_id(), n0 = 16 * blockIdx.x;
+  f32x4_t v;
+  if (!dense_tile(v, a.w_up + (long long)n0 * a.L, 16, a.L, cols_planes(a.yn, a.T, a.L), part)) return;
+  v = plane_sum(v);
+  const int col = lane & 15, t = col / 3;
+  if (col != 3 * t || t >= a.T) return;
+  float ss = 0.f;
+  for (int q = 0; q < nb_cmb; ++q) ss += a.ss[t * nb_cmb + q];
+  v = v * (1.0f / sqrtf(ss / (float)a.L + a.eps));
+  const long long o = (long long)t * a.H + n0 + 4 * (lane >> 4);
+  if (a.S > 0) v += *reinterpret_cast<const f32x4_t *>(a.sd + o);
+  *reinterpret_cast<f32x4_t *>(a.out + o) = v;
 }
 
 }  // namespace
 
-static_assert(FEW_COUNTERS > C_CMB, "every counter is cleared");
+// LDS of an expert kernel's columns, and of the shared experts' sums beside it
+static size_t columns_bytes(int T, int K) {
+  const int ng = (K / 128 + D - 1) / D;
+  const size_t b = (size_t)3 * (T < FEW_ROWS ? T : FEW_ROWS) * ng * D * 256;
+  return b > FNW * 64 * 16 ? b : FNW * 64 * 16;
+}
 
 hipError_t launch_few(const FewArgs &a, hipStream_t st) {
   int dev = 0;
@@ -501,9 +538,29 @@ hipError_t launch_few(const FewArgs &a, hipStream_t st) {
     cus[dev].store(ncu);
   }
   hipLaunchKernelGGL(few_front_kernel, dim3((unsigned)((a.E + 15) / 16 + a.L / 16)), dim3(FTHR), 0, st, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(few_layer_kernel, dim3((unsigned)(2 * ncu)), dim3(FTHR), 0, st, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(few_shared_kernel, dim3((unsigned)(1 + a.S / 8)), dim3(FTHR), 0, st, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  // two work-groups a CU where their columns fit
+  auto groups = [&](size_t lds) { return ncu * (lds <= 80 * 1024 ? 2 : 1); };
+  const size_t l1 = columns_bytes(a.T, a.L), l2 = columns_bytes(a.T, a.I);
+  if (l1 > 64 * 1024)
+    if ((e = hipFuncSetAttribute(reinterpret_cast<const void *>(&few_expert_kernel<true>),
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)l1)) != hipSuccess)
+      return e;
+  if (l2 > 64 * 1024)
+    if ((e = hipFuncSetAttribute(reinterpret_cast<const void *>(&few_expert_kernel<false>),
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)l2)) != hipSuccess)
+      return e;
+  hipLaunchKernelGGL(few_expert_kernel<true>, dim3((unsigned)groups(l1)), dim3(FTHR), l1, st, a, groups(l1));
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(few_expert_kernel<false>, dim3((unsigned)(groups(l2) + a.H / 16 * (a.S > 0))), dim3(FTHR), l2, st, a,
+                     groups(l2));
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const int nb = (a.L + CMB - 1) / CMB;
+  hipLaunchKernelGGL(few_combine_kernel, dim3((unsigned)nb, (unsigned)a.T), dim3(64), 0, st, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(few_up_kernel, dim3((unsigned)(a.H / 16)), dim3(FTHR), 0, st, a, nb);
   return hipGetLastError();
 }
 

@@ -230,15 +230,18 @@ hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, h
 
 // ---- the layer for a few tokens
 constexpr int FEW_MAX_T = 4;
-constexpr int FEW_COUNTERS = 256;    // int32, cleared by the first kernel
 constexpr int FEW_MAX_PAIRS = FEW_MAX_T * 32;  // (token, expert) pairs
-// the chosen experts, each once, with the pairs (token * k + slot) that use it
+constexpr int FEW_ROWS = 2;                    // pairs of an entry
+// the chosen experts with the pairs (token * k + slot) that use them
+struct FewEntry {
+  int32_t expert, npair, pair[FEW_ROWS];
+};
 struct FewList {
   int32_t n;
-  int32_t expert[FEW_MAX_PAIRS];
-  int32_t npair[FEW_MAX_PAIRS];
-  int32_t pair[FEW_MAX_PAIRS][FEW_MAX_T];
+  FewEntry entry[FEW_MAX_PAIRS];
 };
+// longest rows of an expert product: FEW_ROWS pairs' columns stay in LDS
+constexpr int FEW_MAX_K = 12288;
 struct FewArgs {
   int T, H, L, E, k, I, S;
   float beta, beta_lin, eps;
@@ -249,9 +252,7 @@ struct FewArgs {
   float *topk_w;
   float *out;
   // workspace; z, hs, h and yn as three bf16 planes per row
-  int32_t *counters;
   FewList *list;
-  int32_t *ids;
   float *wts, *logits, *ss, *sd, *y;
   uint16_t *z, *hs, *h, *yn;
 };

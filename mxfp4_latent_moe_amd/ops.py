@@ -496,7 +496,7 @@ class LatentMoE:
         return b
 
     def forward_few(self, x: torch.Tensor, stream=None) -> dict:
-        """The layer for up to MOE_FEW_MAX_T tokens (x [T, H] bf16) as one call of two kernels on one stream: for
+        """The layer for up to MOE_FEW_MAX_T tokens (x [T, H] bf16) as one call of six kernels on one stream: for
         single tokens and drafts, where the time of forward() goes into the steps between the weight streams.
         Returns the buffers "out", "topk_ids" and "topk_w" of T tokens (not those of forward(); the next call with
         as many tokens overwrites them, so calls on several streams at once need a layer object each).  Products

@@ -128,8 +128,10 @@ def test_layer_few(lib):
         assert call(**{name: None}) == EINVAL, name
         assert call(**{name: FAKE + 1}) == EINVAL, name
     for bad in (dict(T=_lib.MOE_FEW_MAX_T + 1), dict(s=_shape(hidden=7000)), dict(s=_shape(n_experts=2048)),
-                dict(s=_shape(latent=128 * 513))):
+                dict(s=_shape(latent=128 * 97)), dict(s=_shape(inter=128 * 97)), dict(s=_shape(hidden=128 * 513)),
+                dict(s=_shape(shared_inter=128 * 257))):
         assert call(**bad) == ENOTSUP, bad
+    assert lib.moe_layer_few_workspace_bytes(_shape(latent=128 * 96, inter=128 * 96, hidden=128 * 512), 4) > 0
     assert call(wsb=ws - 1) == EWS
     assert lib.moe_layer_few_workspace_bytes(s, 0) == 0 and lib.moe_layer_few_workspace_bytes(s, 5) == 0
     # without shared experts their tensors are not looked at

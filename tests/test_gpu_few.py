@@ -109,6 +109,18 @@ def test_against_oracle(mx, sh, T):
     assert torch.equal(b["out"], first)
 
 
+@pytest.mark.parametrize("sh", [LayerShape(128, 12288, 6, 2, 128, 1, 128), LayerShape(128, 128, 6, 3, 12288, 0, 0)],
+                         ids=["latent", "inter"])
+def test_longest_rows(mx, sh):
+    """The longest rows whose columns stay in LDS: one work-group a CU."""
+    say(f"case: few tokens {sh}")
+    dense, bias, stack = make(sh, seed=3)
+    moe = mx.LatentMoE(mx.shape_of(sh), upload(dense, bias, stack), DEV)
+    for T in (1, 4):
+        x = tokens(sh, T, seed=30 + T)
+        check(moe.forward_few(to_dev_bf16(x, DEV)), oracle(x, dense, bias, stack, sh), x, moe)
+
+
 def test_matches_the_chain_of_calls(mx):
     sh = SHAPES[4]
     dense, bias, stack = make(sh, seed=11)
@@ -126,7 +138,8 @@ def test_matches_the_chain_of_calls(mx):
 
 
 def test_tokens_that_share_experts(mx):
-    """Four tokens alike: each chosen expert is read once and serves four columns; rows are equal bit for bit."""
+    """Tokens alike: a chosen expert serves several columns, in one entry of the list or two; rows are equal bit for
+    bit."""
     sh = SHAPES[1]
     say("case: few tokens, all alike")
     dense, bias, stack = make(sh, seed=5)

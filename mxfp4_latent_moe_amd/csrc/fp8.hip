@@ -29,6 +29,18 @@ MOE_DEV bf16x8_t codes_to_bf16(uint32_t a, uint32_t b) {
   return r;
 }
 
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+// 16 rows times 16 columns over a block's 128 codes, scales of one
+MOE_DEV f32x4_t mfma_f8(const u32x4_t (&w)[2], const u32x4_t (&x)[2]) {
+  i32x8_t a, b;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = (int)w[i >> 2][i & 3];
+    b[i] = (int)x[i >> 2][i & 3];
+  }
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+}
+
 // value(s) of an output row, four consecutive columns from n on
 template <typename O>
 MOE_DEV void store_cols(O *row, int n, int N, bool vec, int accumulate, f32x4_t v) {
@@ -162,6 +174,148 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args g) {
   }
 }
 
+// ---- many tokens
+// A work-group of four waves owns 64 MT weight rows and 16 NT tokens; a wave has
+// 16 MT rows and all the tokens.  So no two waves need the same weights: those
+// go from memory straight to registers, one block of 128 ahead, and only the
+// tokens' codes pass through LDS (two buffers, one barrier a block), which
+// halves the reads that bound a tile with both operands in LDS.  Two work-groups
+// a CU cover each other's waits.
+//
+// A row's 128 bytes of a block are eight pieces of 16; piece p of row t lies at
+// position p ^ (t / 2 % 8), so the 16 rows that a quarter wave reads at once,
+// two to a 256-byte line of LDS, fall on different banks.
+//
+// F8: a block's sum by the 8-bit instruction, from zero, then times both scales
+// onto the fp32 sum.  Otherwise the codes go through the bf16 instruction.
+template <int MT, int NT, bool F8, bool E8, typename O>
+__global__ __launch_bounds__(256, 2) void fp8_tile_kernel(Fp8Args g, int tiles_n, int tiles_t) {
+  constexpr int TN = 64 * MT, TT = 16 * NT;  // tile
+  constexpr int PIECES = TT * 8 / 256;       // 16-byte pieces of the tokens' codes a thread moves
+  __shared__ u32x4_t lx[2][TT * 8];
+  __shared__ float ls[2][TT];
+  const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int id = xcd_logical(tiles_n * tiles_t);
+  if (id < 0) return;
+  // eight row tiles next to each other, then the next tokens: what an XCD works
+  // on at a time is near square
+  const int per = 8 * tiles_t, grp = id / per, in = id - grp * per, gn = min(8, tiles_n - 8 * grp);
+  const int n0 = (8 * grp + in % gn) * TN, t0 = in / gn * TT;
+  const int K = g.K, kb = (K + 127) / 128;
+  const int nw = n0 + 16 * MT * wave;  // the wave's rows
+  const int nrows = min(max(g.N - nw, 0), 16 * MT), ntok = min(TT, g.T - t0);
+  // rows and tokens past the end are out of range: zeros
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + (long long)min(nw, g.N - 1) * K, (uint32_t)nrows * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + t0 * g.ldx, (uint32_t)((ntok - 1) * g.ldx + K));
+  const __amdgpu_buffer_rsrc_t sr = make_rsrc(g.sx + t0 * g.ldsx, (uint32_t)((ntok - 1) * g.ldsx + kb));
+  const uint32_t wo = (uint32_t)r16 * (uint32_t)K + 16 * kg;
+  const int xrow = tid >> 3, xp = tid & 7;
+  const uint32_t xo = (uint32_t)(xrow * g.ldx) + 16 * xp, xstep = (uint32_t)(32 * g.ldx);
+  const uint32_t so = (uint32_t)((tid & (TT - 1)) * g.ldsx);
+  const long long srow = (long long)(min(nw, g.N - 1) / 128) * kb;  // 16 MT divides 128
+
+  struct Block {
+    u32x4_t w[MT][2], x[PIECES];
+    uint32_t s;
+  };
+  auto request = [&](Block &q, int b) {
+    b = min(b, kb - 1);  // past the last block that one again, unused
+    const uint32_t k0 = 128u * b, none = 0x70000000u;
+    // a block that ends inside: pieces past K read out of range
+    const uint32_t d[2] = {k0 + 16 * kg < (uint32_t)K ? 0u : none, k0 + 16 * kg + 64 < (uint32_t)K ? 64u : none};
+    const uint32_t dx = k0 + 16 * xp < (uint32_t)K ? 0u : none;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) q.w[m][h] = buf_load16(wr, wo + 16u * m * (uint32_t)K + d[h], k0);
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) q.x[u] = buf_load16(xr, xo + u * xstep + dx, k0);
+    q.s = __builtin_amdgcn_raw_buffer_load_b8(sr, so, b, 0);
+  };
+  auto put = [&](const Block &q, int buf) {
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+      const int t = xrow + 32 * u;
+      lx[buf][8 * t + (xp ^ (t >> 1 & 7))] = q.x[u];
+    }
+    if (tid < TT) ls[buf][tid] = e8m0_to_float(q.s);
+  };
+  auto weight_scale = [&](int b) {
+    if constexpr (E8) {
+      const uint32_t e = static_cast<const uint8_t *>(g.sw)[srow + b];
+      // 2^(e - 127); byte 0 is the subnormal 2^-127, 255 is NaN
+      return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
+    } else {
+      return static_cast<const float *>(g.sw)[srow + b];
+    }
+  };
+
+  f32x4_t acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Block &q, int buf, float sw) {
+    bf16x8_t wb[F8 ? 1 : MT][4];
+    if constexpr (!F8) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) wb[m][c] = codes_to_bf16(q.w[m][c >> 1][2 * (c & 1)], q.w[m][c >> 1][2 * (c & 1) + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int t = 16 * i + r16, sz = t >> 1 & 7;
+      u32x4_t x[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x[h] = lx[buf][8 * t + ((kg + 4 * h) ^ sz)];
+      const float sc = ls[buf][t] * sw;
+      f32x4_t p[MT];
+      if constexpr (F8) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) p[m] = mfma_f8(q.w[m], x);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bf16x8_t xb = codes_to_bf16(x[c >> 1][2 * (c & 1)], x[c >> 1][2 * (c & 1) + 1]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) p[m] = mfma_16x16x32(wb[m][c], xb, c == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : p[m]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[m][i][r] = fmaf(p[m][r], sc, acc[m][i][r]);
+    }
+  };
+
+  Block q[2];
+  request(q[0], 0);
+  put(q[0], 0);
+  __syncthreads();
+  for (int b = 0; b < kb; b += 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float sw = b + h < kb ? weight_scale(b + h) : 0.f;
+      request(q[h ^ 1], b + h + 1);
+      __builtin_amdgcn_sched_barrier(0);  // on its way before the products
+      if (b + h < kb) multiply(q[h], h, sw);
+      put(q[h ^ 1], h ^ 1);
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int t = 16 * i + r16;
+    if (t < ntok)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        store_cols<O>(static_cast<O *>(g.out) + (t0 + t) * g.ldo, nw + 16 * m + 4 * kg, g.N, g.vec_out, g.accumulate,
+                      acc[m][i]);
+  }
+}
+
 template <int NT, int MT, int NW, int U>
 void stream_by_type(const Fp8Args &g, bool e8, bool out_bf16, hipStream_t st) {
   const dim3 gr((unsigned)((g.N + 16 * MT - 1) / (16 * MT)), (unsigned)((g.T + 16 * NT - 1) / (16 * NT))), blk(64 * NW);
@@ -174,12 +328,23 @@ void stream_by_type(const Fp8Args &g, bool e8, bool out_bf16, hipStream_t st) {
   }
 }
 
+template <int MT, int NT, bool F8, typename O>
+void tile_by_type(const Fp8Args &g, bool e8, hipStream_t st) {
+  const int tn = (g.N + 64 * MT - 1) / (64 * MT), tt = (g.T + 16 * NT - 1) / (16 * NT);
+  const dim3 gr((unsigned)((tn * tt + 7) / 8 * 8)), blk(256);
+  if (e8) hipLaunchKernelGGL((fp8_tile_kernel<MT, NT, F8, true, O>), gr, blk, 0, st, g, tn, tt);
+  else hipLaunchKernelGGL((fp8_tile_kernel<MT, NT, F8, false, O>), gr, blk, 0, st, g, tn, tt);
+}
+
 }  // namespace
 
 size_t fp8_workspace_bytes(int T, int N, int K) { return 0; }
 
 hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, hipStream_t st) {
-  if (g.T <= 16) stream_by_type<1, 1, 8, 4>(g, e8, out_bf16, st);
+  if (g.T > 64) {
+    if (out_bf16) tile_by_type<4, 8, true, uint16_t>(g, e8, st);
+    else tile_by_type<2, 8, false, float>(g, e8, st);
+  } else if (g.T <= 16) stream_by_type<1, 1, 8, 4>(g, e8, out_bf16, st);
   else if (g.T <= 32) stream_by_type<2, 1, 8, 2>(g, e8, out_bf16, st);
   else stream_by_type<4, 2, 8, 1>(g, e8, out_bf16, st);
   return hipGetLastError();

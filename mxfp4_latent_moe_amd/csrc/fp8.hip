@@ -11,6 +11,8 @@
 // codes by 5e-5 (measured; products that fit the window are exact).  fp32
 // outputs therefore take the codes as bf16 (exact) through the bf16
 // instruction, whose sums are fp32 (1e-8 and 8e-8 on the same operands).
+#include <algorithm>
+
 #include "kernels.h"
 #include "quant8.h"
 
@@ -175,80 +177,117 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args g) {
 }
 
 // ---- many tokens
-// A work-group of four waves owns 64 MT weight rows and 16 NT tokens; a wave has
-// 16 MT rows and all the tokens.  So no two waves need the same weights: those
-// go from memory straight to registers, one block of 128 ahead, and only the
-// tokens' codes pass through LDS (two buffers, one barrier a block), which
-// halves the reads that bound a tile with both operands in LDS.  Two work-groups
-// a CU cover each other's waits.
+// A work-group of eight waves owns 64 MT weight rows and 256 tokens, a wave of
+// it 16 MT rows and 128 tokens; K may be split over work-groups, whose sums
+// fp8_join_kernel adds.  Both operands pass through two LDS stages of one block
+// of 128, filled by direct loads of rows' whole 128 bytes, two a wave between
+// the products of the first half of a block.
 //
-// A row's 128 bytes of a block are eight pieces of 16; piece p of row t lies at
-// position p ^ (t / 2 % 8), so the 16 rows that a quarter wave reads at once,
-// two to a 256-byte line of LDS, fall on different banks.
+// A row's 128 bytes are eight pieces of 16; piece p of row r lies at position
+// p ^ (r / 2 % 8), so the 16 rows that a quarter wave reads at once, two to a
+// 256-byte line of LDS, fall on different banks.
 //
 // F8: a block's sum by the 8-bit instruction, from zero, then times both scales
-// onto the fp32 sum.  Otherwise the codes go through the bf16 instruction.
-template <int MT, int NT, bool F8, bool E8, typename O>
-__global__ __launch_bounds__(256, 2) void fp8_tile_kernel(Fp8Args g, int tiles_n, int tiles_t) {
-  constexpr int TN = 64 * MT, TT = 16 * NT;  // tile
-  constexpr int PIECES = TT * 8 / 256;       // 16-byte pieces of the tokens' codes a thread moves
-  __shared__ u32x4_t lx[2][TT * 8];
-  __shared__ float ls[2][TT];
-  const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int id = xcd_logical(tiles_n * tiles_t);
-  if (id < 0) return;
-  // eight row tiles next to each other, then the next tokens: what an XCD works
-  // on at a time is near square
-  const int per = 8 * tiles_t, grp = id / per, in = id - grp * per, gn = min(8, tiles_n - 8 * grp);
-  const int n0 = (8 * grp + in % gn) * TN, t0 = in / gn * TT;
-  const int K = g.K, kb = (K + 127) / 128;
-  const int nw = n0 + 16 * MT * wave;  // the wave's rows
-  const int nrows = min(max(g.N - nw, 0), 16 * MT), ntok = min(TT, g.T - t0);
-  // rows and tokens past the end are out of range: zeros
-  const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + (long long)min(nw, g.N - 1) * K, (uint32_t)nrows * (uint32_t)K);
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + t0 * g.ldx, (uint32_t)((ntok - 1) * g.ldx + K));
-  const __amdgpu_buffer_rsrc_t sr = make_rsrc(g.sx + t0 * g.ldsx, (uint32_t)((ntok - 1) * g.ldsx + kb));
-  const uint32_t wo = (uint32_t)r16 * (uint32_t)K + 16 * kg;
-  const int xrow = tid >> 3, xp = tid & 7;
-  const uint32_t xo = (uint32_t)(xrow * g.ldx) + 16 * xp, xstep = (uint32_t)(32 * g.ldx);
-  const uint32_t so = (uint32_t)((tid & (TT - 1)) * g.ldsx);
-  const long long srow = (long long)(min(nw, g.N - 1) / 128) * kb;  // 16 MT divides 128
+// onto the fp32 sum, between the next tokens' products.  Otherwise the codes go
+// through the bf16 instruction.
+//
+// 4096 x 6144 x 7168 takes 196 us to bf16 (1.84 PFLOP/s) and 339 to fp32 (1.06).
+// What bounds the first: products and LDS reads alone take 93 us (3.9 PFLOP/s);
+// the multiply-adds with the scales, which do not overlap the 8-bit
+// instruction (it leaves the vector unit few register reads), bring that to
+// 185, the loads to 196; a turn and a half of tiles on 256 CUs cost a quarter
+// of it.  Tried and slower: weights straight to the registers of the one wave
+// that needs them (291 us: such a load touches 16 rows for 64 bytes each), 192
+// rows a tile in two whole turns (205), all of a block's loads at its start (208).
+constexpr int TNT = 8;   // 16-token tiles of a wave
+constexpr int SCB = 8;   // blocks whose scales are in LDS at a time
 
-  struct Block {
-    u32x4_t w[MT][2], x[PIECES];
-    uint32_t s;
+// 16 bytes of LDS at a + O, issued without waiting
+template <int O>
+MOE_DEV void tread(uint32_t a, u32x4_t &v) {
+  static_assert(O >= 0 && O < 65536, "offset field");
+  asm volatile("ds_read_b128 %0, %1 offset:%2" : "=&v"(v) : "v"(a), "n"(O) : "memory");
+}
+template <int N>
+MOE_DEV void twait() {
+  asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(N) : "memory");
+}
+// ties a register to the wait before: its users stay behind it
+MOE_DEV void ttie(u32x4_t &v) { asm volatile("" : "+v"(v)); }
+
+template <int MT>
+struct TileLds {
+  uint8_t w[2][64 * MT * 128], x[2][256 * 128];  // codes by stage
+  // products of the scales, by block, the tile's block of rows, half of the
+  // tokens, token % 16 and the wave's tile of tokens
+  float s[SCB][2][2][16][TNT];
+};
+
+template <int MT, bool F8, bool E8, typename O>
+MOE_DEV void fp8_tile(const Fp8Args &g, int tiles_n, int tiles_t, int splits, float *partial, TileLds<MT> &l) {
+  constexpr int NT = TNT, TN = 64 * MT, TT = 256;
+  constexpr int WL = TN / 64, XL = TT / 64;  // direct loads of a wave per block, 8 rows each
+  const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 3, wt = wave >> 2;
+  const int work = xcd_logical(tiles_n * tiles_t * splits);
+  if (work < 0) return;
+  // a few row tiles next to each other, then the next tokens: what an XCD works
+  // on at a time is near square
+  const int split = work / (tiles_n * tiles_t), id = work - split * tiles_n * tiles_t;
+  const int per = 4 * tiles_t, grp = id / per, in = id - grp * per, gn = min(4, tiles_n - 4 * grp);
+  const int n0 = (4 * grp + in % gn) * TN, t0 = in / gn * TT;
+  const int K = g.K, kb = (K + 127) / 128;
+  const int first = (int)((long long)split * kb / splits), nblk = (int)((long long)(split + 1) * kb / splits) - first;
+  const int nrows = min(TN, g.N - n0), ntok = min(TT, g.T - t0);
+  // rows and tokens past the end are out of range: zeros
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(g.w + (long long)n0 * K, (uint32_t)nrows * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + t0 * g.ldx, (uint32_t)((ntok - 1) * g.ldx + K));
+  // direct load u of this wave fills rows 8 (8 u + wave) ..: lane i's 16 bytes
+  // land at position i % 8 of row i / 8; the swizzle repeats every 16 rows, so
+  // the piece is the same for every u
+  const int r0 = 8 * wave + (lane >> 3), piece = (lane & 7) ^ (r0 >> 1 & 7);
+  const uint32_t wo = (uint32_t)r0 * (uint32_t)K + 16 * piece, xo = (uint32_t)(r0 * g.ldx) + 16 * piece;
+  const uint32_t wstep = 64u * (uint32_t)K, xstep = (uint32_t)(64 * g.ldx);
+  // load u of block b of this split: the weights' first, then the tokens'
+  auto request = [&](int stage, int b, auto uc) {
+    constexpr int u = decltype(uc)::value;
+    const uint32_t k0 = 128u * min(first + b, kb - 1);  // past the last block that one again, unused
+    // of a block that ends inside, pieces past K read out of range
+    const uint32_t out = k0 + 16 * piece < (uint32_t)K ? 0u : 0x70000000u;
+    if constexpr (u < WL)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_void *)(l.w[stage] + (8 * u + wave) * 1024), 16,
+                                               wo + u * wstep + out, k0, 0, 0);
+    else if constexpr (u < WL + XL)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void *)(l.x[stage] + (8 * (u - WL) + wave) * 1024), 16,
+                                               xo + (u - WL) * xstep + out, k0, 0, 0);
   };
-  auto request = [&](Block &q, int b) {
-    b = min(b, kb - 1);  // past the last block that one again, unused
-    const uint32_t k0 = 128u * b, none = 0x70000000u;
-    // a block that ends inside: pieces past K read out of range
-    const uint32_t d[2] = {k0 + 16 * kg < (uint32_t)K ? 0u : none, k0 + 16 * kg + 64 < (uint32_t)K ? 64u : none};
-    const uint32_t dx = k0 + 16 * xp < (uint32_t)K ? 0u : none;
+  // the scales of blocks b0 .. b0 + SCB / 2 - 1, a token and half of the blocks
+  // a thread: requested by one step, put into their half of the buffer by the next
+  constexpr int SU = SCB / 4, SH = TN > 128 ? 2 : 1;
+  const int st = tid & 255, su = wave >> 2;
+  uint32_t sx[SU], sw[SU][SH];
+  auto request_scales = [&](int b0) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int u = 0; u < SU; ++u) {
+      const int at = min(first + b0 + su + 2 * u, kb - 1);
+      sx[u] = g.sx[(t0 + min(st, ntok - 1)) * g.ldsx + at];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) q.w[m][h] = buf_load16(wr, wo + 16u * m * (uint32_t)K + d[h], k0);
-#pragma unroll
-    for (int u = 0; u < PIECES; ++u) q.x[u] = buf_load16(xr, xo + u * xstep + dx, k0);
-    q.s = __builtin_amdgcn_raw_buffer_load_b8(sr, so, b, 0);
-  };
-  auto put = [&](const Block &q, int buf) {
-#pragma unroll
-    for (int u = 0; u < PIECES; ++u) {
-      const int t = xrow + 32 * u;
-      lx[buf][8 * t + (xp ^ (t >> 1 & 7))] = q.x[u];
+      for (int h = 0; h < SH; ++h) {
+        const long long wi = (long long)(min(n0 + 128 * h, g.N - 1) / 128) * kb + at;
+        if constexpr (E8) sw[u][h] = static_cast<const uint8_t *>(g.sw)[wi];
+        else sw[u][h] = static_cast<const uint32_t *>(g.sw)[wi];
+      }
     }
-    if (tid < TT) ls[buf][tid] = e8m0_to_float(q.s);
   };
-  auto weight_scale = [&](int b) {
-    if constexpr (E8) {
-      const uint32_t e = static_cast<const uint8_t *>(g.sw)[srow + b];
-      // 2^(e - 127); byte 0 is the subnormal 2^-127, 255 is NaN
-      return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
-    } else {
-      return static_cast<const float *>(g.sw)[srow + b];
-    }
+  auto put_scales = [&](int b0) {
+#pragma unroll
+    for (int u = 0; u < SU; ++u)
+#pragma unroll
+      for (int h = 0; h < SH; ++h) {
+        // a byte is 2^(e - 127); 0 is the subnormal 2^-127, 255 is NaN
+        const uint32_t e = sw[u][h], f = !E8 ? e : e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23;
+        l.s[(b0 + su + 2 * u) % SCB][h][st >> 7][st & 15][st >> 4 & 7] = e8m0_to_float(sx[u]) * __uint_as_float(f);
+      }
   };
 
   f32x4_t acc[MT][NT];
@@ -256,64 +295,150 @@ __global__ __launch_bounds__(256, 2) void fp8_tile_kernel(Fp8Args g, int tiles_n
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const Block &q, int buf, float sw) {
+  const uint32_t sz = r16 >> 1;
+  uint32_t wa[2], xa[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t at = 128 * r16 + 16 * ((kg + 4 * q) ^ sz);
+    wa[q] = lds_addr(l.w[0]) + 2048 * MT * wn + at;
+    xa[q] = lds_addr(l.x[0]) + 16384 * wt + at;
+  }
+  const uint32_t sa = lds_addr(reinterpret_cast<const uint8_t *>(l.s[0][16 * MT * wn >= 128][wt][r16]));
+
+  static_for<WL + XL>([&](auto uc) { request(0, 0, uc); });
+  request_scales(0);
+  put_scales(0);
+  auto step = [&](auto hc, int b) {
+    constexpr int h = decltype(hc)::value;
+    // this block has landed, and every wave is done with the one before
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    __syncthreads();
+    if (b % (SCB / 2) == 0) request_scales(b + SCB / 2);
+    else if (b % (SCB / 2) == 1) put_scales(b - 1 + SCB / 2);  // whose half nobody reads any more
+    u32x4_t sc[2], w[MT][2], x[2][2];
+    auto read_x = [&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      tread<h * TT * 128 + 2048 * i>(xa[0], x[i & 1][0]);
+      tread<h * TT * 128 + 2048 * i>(xa[1], x[i & 1][1]);
+    };
+    tread<0>(sa + b % SCB * 2048, sc[0]);
+    tread<16>(sa + b % SCB * 2048, sc[1]);
+    read_x(std::integral_constant<int, 0>{});
+    static_for<MT>([&](auto mc) {
+      constexpr int m = decltype(mc)::value;
+      tread<h * TN * 128 + 2048 * m>(wa[0], w[m][0]);
+      tread<h * TN * 128 + 2048 * m>(wa[1], w[m][1]);
+    });
+    read_x(std::integral_constant<int, 1>{});
+    f32x4_t p[2][MT];
     bf16x8_t wb[F8 ? 1 : MT][4];
-    if constexpr (!F8) {
+    auto add = [&](int i, int m) {
+      const float f = __uint_as_float(sc[i >> 2][i & 3]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) wb[m][c] = codes_to_bf16(q.w[m][c >> 1][2 * (c & 1)], q.w[m][c >> 1][2 * (c & 1) + 1]);
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int t = 16 * i + r16, sz = t >> 1 & 7;
-      u32x4_t x[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) x[h] = lx[buf][8 * t + ((kg + 4 * h) ^ sz)];
-      const float sc = ls[buf][t] * sw;
-      f32x4_t p[MT];
+      for (int r = 0; r < 4; ++r) acc[m][i][r] = fmaf(p[i & 1][m][r], f, acc[m][i][r]);
+    };
+    static_for<NT>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
+      if constexpr (i > 0) {
+        if constexpr (i + 1 < NT) {
+          read_x(std::integral_constant<int, i + 1>{});
+          twait<2>();
+        } else {
+          twait<0>();
+        }
+        ttie(x[i & 1][0]);
+        ttie(x[i & 1][1]);
+      }
+      if constexpr (i < (WL + XL + 1) / 2) {
+        request(h ^ 1, b + 1, std::integral_constant<int, 2 * i>{});
+        request(h ^ 1, b + 1, std::integral_constant<int, 2 * i + 1>{});
+      }
       if constexpr (F8) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) p[m] = mfma_f8(q.w[m], x);
+        static_for<MT>([&](auto mc) {
+          constexpr int m = decltype(mc)::value;
+          if constexpr (i == 0) {  // the weights as they come
+            twait<2 * (MT - 1 - m) + 2>();
+            if constexpr (m == 0) {
+              ttie(sc[0]);
+              ttie(sc[1]);
+              ttie(x[0][0]);
+              ttie(x[0][1]);
+            }
+            ttie(w[m][0]);
+            ttie(w[m][1]);
+          }
+          p[i & 1][m] = mfma_f8(w[m], x[i & 1]);
+          if constexpr (i > 0) add(i - 1, m);
+        });
       } else {
+        if constexpr (i == 0) {
+          twait<2>();
+          ttie(sc[0]);
+          ttie(sc[1]);
+          ttie(x[0][0]);
+          ttie(x[0][1]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            ttie(w[m][0]);
+            ttie(w[m][1]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) wb[m][c] = codes_to_bf16(w[m][c >> 1][2 * (c & 1)], w[m][c >> 1][2 * (c & 1) + 1]);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const bf16x8_t xb = codes_to_bf16(x[c >> 1][2 * (c & 1)], x[c >> 1][2 * (c & 1) + 1]);
+          const bf16x8_t xb = codes_to_bf16(x[i & 1][c >> 1][2 * (c & 1)], x[i & 1][c >> 1][2 * (c & 1) + 1]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) p[m] = mfma_16x16x32(wb[m][c], xb, c == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : p[m]);
+          for (int m = 0; m < MT; ++m)
+            p[i & 1][m] = mfma_16x16x32(wb[m][c], xb, c == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : p[i & 1][m]);
+        }
+        if constexpr (i > 0) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) add(i - 1, m);
         }
       }
+    });
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[m][i][r] = fmaf(p[m][r], sc, acc[m][i][r]);
-    }
+    for (int m = 0; m < MT; ++m) add(NT - 1, m);
   };
-
-  Block q[2];
-  request(q[0], 0);
-  put(q[0], 0);
-  __syncthreads();
-  for (int b = 0; b < kb; b += 2) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float sw = b + h < kb ? weight_scale(b + h) : 0.f;
-      request(q[h ^ 1], b + h + 1);
-      __builtin_amdgcn_sched_barrier(0);  // on its way before the products
-      if (b + h < kb) multiply(q[h], h, sw);
-      put(q[h ^ 1], h ^ 1);
-      __syncthreads();
-    }
+  for (int b = 0; b < nblk; b += 2) {
+    step(std::integral_constant<int, 0>{}, b);
+    if (b + 1 < nblk) step(std::integral_constant<int, 1>{}, b + 1);
   }
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  const int nw = n0 + 16 * MT * wn, ldp = (g.N + 3) & ~3;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int t = 16 * i + r16;
+    const int t = 128 * wt + 16 * i + r16;
     if (t < ntok)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        store_cols<O>(static_cast<O *>(g.out) + (t0 + t) * g.ldo, nw + 16 * m + 4 * kg, g.N, g.vec_out, g.accumulate,
-                      acc[m][i]);
+      for (int m = 0; m < MT; ++m) {
+        const int n = nw + 16 * m + 4 * kg;
+        if (splits > 1) store_cols<float>(partial + ((long long)split * g.T + t0 + t) * ldp, n, ldp, true, 0, acc[m][i]);
+        else store_cols<O>(static_cast<O *>(g.out) + (t0 + t) * g.ldo, n, g.N, g.vec_out, g.accumulate, acc[m][i]);
+      }
   }
+}
+
+template <int MT, bool F8, bool E8, typename O>
+__global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8Args g, int tiles_n, int tiles_t, int splits,
+                                                          float *partial) {
+  __shared__ __attribute__((aligned(1024))) TileLds<MT> l;
+  fp8_tile<MT, F8, E8, O>(g, tiles_n, tiles_t, splits, partial, l);
+}
+
+// the splits' sums in order, four columns a thread
+template <typename O>
+__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Args g, int splits, const float *partial) {
+  const int per = (g.N + 3) / 4;  // rows of partial are whole groups of four
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, stride = (long long)g.T * per;
+  if (i >= stride) return;
+  const int t = (int)(i / per), n = 4 * (int)(i - (long long)t * per);
+  const f32x4_t *p = reinterpret_cast<const f32x4_t *>(partial) + i;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) v += p[s * stride];
+  store_cols<O>(static_cast<O *>(g.out) + t * g.ldo, n, g.N, g.vec_out, g.accumulate, v);
 }
 
 template <int NT, int MT, int NW, int U>
@@ -328,25 +453,68 @@ void stream_by_type(const Fp8Args &g, bool e8, bool out_bf16, hipStream_t st) {
   }
 }
 
-template <int MT, int NT, bool F8, typename O>
-void tile_by_type(const Fp8Args &g, bool e8, hipStream_t st) {
-  const int tn = (g.N + 64 * MT - 1) / (64 * MT), tt = (g.T + 16 * NT - 1) / (16 * NT);
-  const dim3 gr((unsigned)((tn * tt + 7) / 8 * 8)), blk(256);
-  if (e8) hipLaunchKernelGGL((fp8_tile_kernel<MT, NT, F8, true, O>), gr, blk, 0, st, g, tn, tt);
-  else hipLaunchKernelGGL((fp8_tile_kernel<MT, NT, F8, false, O>), gr, blk, 0, st, g, tn, tt);
+template <int MT, bool F8, typename O>
+void tile_by_type(const Fp8Args &g, bool e8, int splits, float *partial, hipStream_t st) {
+  const int tn = (g.N + 64 * MT - 1) / (64 * MT), tt = (g.T + 255) / 256;
+  const dim3 gr((unsigned)((tn * tt * splits + 7) / 8 * 8)), blk(512);
+  if (e8) hipLaunchKernelGGL((fp8_tile_kernel<MT, F8, true, O>), gr, blk, 0, st, g, tn, tt, splits, partial);
+  else hipLaunchKernelGGL((fp8_tile_kernel<MT, F8, false, O>), gr, blk, 0, st, g, tn, tt, splits, partial);
+  if (splits > 1)
+    hipLaunchKernelGGL(fp8_join_kernel<O>, dim3((unsigned)(((long long)g.T * ((g.N + 3) / 4) + 255) / 256)), dim3(256),
+                       0, st, g, splits, partial);
 }
 
 }  // namespace
 
-size_t fp8_workspace_bytes(int T, int N, int K) { return 0; }
+// How the tile kernel splits K: where the tiles are fewer than the CUs, into
+// about one work-group a CU, of four blocks at least; and what the product then
+// takes, in us: 10 for the kernel's ends, 1.1 + rows / 400 for a block, and the
+// parts' sums written and read at 4 TB/s.
+struct TilePlan {
+  int splits;
+  double us;
+};
+static TilePlan tile_plan(int T, int N, int K, bool out_bf16) {
+  const int rows = out_bf16 ? 256 : 128;
+  const long long tiles = (long long)((N + rows - 1) / rows) * ((T + 255) / 256);
+  const int kb = (K + 127) / 128;
+  const int s = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(256 / tiles, kb / 4), 16));
+  const double rounds = (double)((tiles * s + 255) / 256);
+  return {s, 10 + (1.1 + rows / 400.0) * ((kb + s - 1) / s) * rounds + (s > 1 ? 2e-6 * s * T * N : 0.0)};
+}
+// Whether the stream kernel is faster: its work-groups of 32 rows and 64 tokens
+// take 0.43 us a block, one a CU at a time.  Measured at K = 7168, bf16 out,
+// stream against tiles: 64 tokens and 6144 rows 24 / 22 us, 512 and 895 24 / 29,
+// 128 and 6144 48 / 28, 1024 and 895 46 / 30, 512 and 6144 135 / 47; at K = 512,
+// 300 tokens and 3584 rows, 11 / 17.  Up to 64 tokens it is always taken.
+static bool stream_fits(const TilePlan &tile, int T, int N, int K) {
+  if (T <= 64) return true;
+  const long long groups = (long long)((N + 31) / 32) * ((T + 63) / 64);
+  return 3 + 0.43 * ((K + 127) / 128) * (double)((groups + 255) / 256) <= tile.us;
+}
+
+size_t fp8_workspace_bytes(int T, int N, int K) {
+  size_t need = 0;
+  for (const bool out_bf16 : {false, true}) {
+    const TilePlan p = tile_plan(T, N, K, out_bf16);
+    if (!stream_fits(p, T, N, K) && p.splits > 1) need = std::max(need, (size_t)p.splits * T * ((N + 3) / 4) * 16);
+  }
+  return need;
+}
 
 hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, hipStream_t st) {
-  if (g.T > 64) {
-    if (out_bf16) tile_by_type<4, 8, true, uint16_t>(g, e8, st);
-    else tile_by_type<2, 8, false, float>(g, e8, st);
-  } else if (g.T <= 16) stream_by_type<1, 1, 8, 4>(g, e8, out_bf16, st);
-  else if (g.T <= 32) stream_by_type<2, 1, 8, 2>(g, e8, out_bf16, st);
-  else stream_by_type<4, 2, 8, 1>(g, e8, out_bf16, st);
+  const TilePlan p = tile_plan(g.T, g.N, g.K, out_bf16);
+  if (!stream_fits(p, g.T, g.N, g.K)) {
+    float *partial = static_cast<float *>(ws);
+    if (out_bf16) tile_by_type<4, true, uint16_t>(g, e8, p.splits, partial, st);
+    else tile_by_type<2, false, float>(g, e8, p.splits, partial, st);
+  } else if (g.T <= 16) {
+    stream_by_type<1, 1, 8, 4>(g, e8, out_bf16, st);
+  } else if (g.T <= 32) {
+    stream_by_type<2, 1, 8, 2>(g, e8, out_bf16, st);
+  } else {
+    stream_by_type<4, 2, 8, 1>(g, e8, out_bf16, st);
+  }
   return hipGetLastError();
 }
 

@@ -32,15 +32,16 @@ MOE_DEV bf16x8_t codes_to_bf16(uint32_t a, uint32_t b) {
 }
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-// 16 rows times 16 columns over a block's 128 codes, scales of one
-MOE_DEV f32x4_t mfma_f8(const u32x4_t (&w)[2], const u32x4_t (&x)[2]) {
+// c + 16 rows times 16 columns over a block's 128 codes, times 2^(a - 127) of
+// the row and 2^(b - 127) of the column: bytes 1 and 0 of `scales`
+MOE_DEV f32x4_t mfma_f8(const u32x4_t (&w)[2], const u32x4_t (&x)[2], f32x4_t c, uint32_t scales) {
   i32x8_t a, b;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     a[i] = (int)w[i >> 2][i & 3];
     b[i] = (int)x[i >> 2][i & 3];
   }
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 1, (int)scales, 0, (int)scales);
 }
 
 // value(s) of an output row, four consecutive columns from n on
@@ -177,29 +178,31 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args g) {
 }
 
 // ---- many tokens
-// A work-group of eight waves owns 64 MT weight rows and 256 tokens, a wave of
-// it 16 MT rows and 128 tokens; K may be split over work-groups, whose sums
-// fp8_join_kernel adds.  Both operands pass through two LDS stages of one block
-// of 128, filled by direct loads of rows' whole 128 bytes, two a wave between
-// the products of the first half of a block.
+// A work-group of eight waves owns 64 MT weight rows and 32 NT tokens, a wave of
+// it 16 MT rows and 16 NT tokens; K may be split over work-groups, whose sums
+// fp8_join_kernel adds.  Both operands pass through ST LDS stages of one block
+// of 128, filled by direct loads of rows' whole 128 bytes between the products.
 //
 // A row's 128 bytes are eight pieces of 16; piece p of row r lies at position
 // p ^ (r / 2 % 8), so the 16 rows that a quarter wave reads at once, two to a
 // 256-byte line of LDS, fall on different banks.
 //
-// F8: a block's sum by the 8-bit instruction, from zero, then times both scales
-// onto the fp32 sum, between the next tokens' products.  Otherwise the codes go
+// F8 takes the 8-bit instruction.  With e8m0 weight scales both scales go
+// through it, onto the sum (which keeps fp32's precision there: what the
+// instruction drops is measured against the products, not the sum: measured
+// within 2 units in the sum's last place); fp32 scales multiply a block's sum
+// onto the fp32 sum, between the next tokens' products.  Without F8 the codes go
 // through the bf16 instruction.
 //
-// 4096 x 6144 x 7168 takes 196 us to bf16 (1.84 PFLOP/s) and 339 to fp32 (1.06).
-// What bounds the first: products and LDS reads alone take 93 us (3.9 PFLOP/s);
-// the multiply-adds with the scales, which do not overlap the 8-bit
-// instruction (it leaves the vector unit few register reads), bring that to
-// 185, the loads to 196; a turn and a half of tiles on 256 CUs cost a quarter
-// of it.  Tried and slower: weights straight to the registers of the one wave
-// that needs them (291 us: such a load touches 16 rows for 64 bytes each), 192
-// rows a tile in two whole turns (205), all of a block's loads at its start (208).
-constexpr int TNT = 8;   // 16-token tiles of a wave
+// 4096 x 6144 x 7168: 193 us to bf16 with fp32 scales (1.87 PFLOP/s), 169 with
+// e8m0 scales (2.13), 360 to fp32 (1.0; the library's bf16 product of 8192^3
+// runs at 1.25, its 8-bit one without block scales takes 154 us here).  What
+// bounds the first: the same without the multiply-adds takes 169; without loads
+// and barriers, 165 (products, multiply-adds and LDS reads: the 8-bit
+// instructions alone, fed from LDS one read each, reach 3.0 PFLOP/s, 120 us).
+// Tried and slower: weights straight to the registers of the one wave that needs
+// them (291 us: such a load touches 16 rows for 64 bytes each), 192 rows a tile
+// (205), all of a block's loads at its start (+9).
 constexpr int SCB = 8;   // blocks whose scales are in LDS at a time
 
 // 16 bytes of LDS at a + O, issued without waiting
@@ -215,27 +218,29 @@ MOE_DEV void twait() {
 // ties a register to the wait before: its users stay behind it
 MOE_DEV void ttie(u32x4_t &v) { asm volatile("" : "+v"(v)); }
 
-template <int MT>
+template <int MT, int NT, int ST>
 struct TileLds {
-  uint8_t w[2][64 * MT * 128], x[2][256 * 128];  // codes by stage
-  // products of the scales, by block, the tile's block of rows, half of the
-  // tokens, token % 16 and the wave's tile of tokens
-  float s[SCB][2][2][16][TNT];
+  uint8_t w[ST][64 * MT * 128], x[ST][32 * NT * 128];  // codes by stage
+  // products of the scales, or both bytes, by block, the tile's block of rows,
+  // half of the tokens, token % 16 and the wave's tile of tokens
+  float s[SCB][MT > 2 ? 2 : 1][2][16][NT];
 };
 
-template <int MT, bool F8, bool E8, typename O>
-MOE_DEV void fp8_tile(const Fp8Args &g, int tiles_n, int tiles_t, int splits, float *partial, TileLds<MT> &l) {
-  constexpr int NT = TNT, TN = 64 * MT, TT = 256;
+// tile `work` of tiles_n x tiles_t x splits, of rows from row0 on
+template <int MT, int NT, int ST, bool F8, bool E8, typename O>
+MOE_DEV void fp8_tile(const Fp8Args &g, int work, int row0, int tiles_n, int tiles_t, int splits, float *partial,
+                      TileLds<MT, NT, ST> &l) {
+  constexpr int TN = 64 * MT, TT = 32 * NT;
+  // scales that are all powers of two go through the instruction, onto the sum
+  constexpr bool ACC = F8 && E8;
   constexpr int WL = TN / 64, XL = TT / 64;  // direct loads of a wave per block, 8 rows each
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 3, wt = wave >> 2;
-  const int work = xcd_logical(tiles_n * tiles_t * splits);
-  if (work < 0) return;
   // a few row tiles next to each other, then the next tokens: what an XCD works
   // on at a time is near square
   const int split = work / (tiles_n * tiles_t), id = work - split * tiles_n * tiles_t;
   const int per = 4 * tiles_t, grp = id / per, in = id - grp * per, gn = min(4, tiles_n - 4 * grp);
-  const int n0 = (4 * grp + in % gn) * TN, t0 = in / gn * TT;
+  const int n0 = row0 + (4 * grp + in % gn) * TN, t0 = in / gn * TT;
   const int K = g.K, kb = (K + 127) / 128;
   const int first = (int)((long long)split * kb / splits), nblk = (int)((long long)(split + 1) * kb / splits) - first;
   const int nrows = min(TN, g.N - n0), ntok = min(TT, g.T - t0);
@@ -263,13 +268,13 @@ MOE_DEV void fp8_tile(const Fp8Args &g, int tiles_n, int tiles_t, int splits, fl
   };
   // the scales of blocks b0 .. b0 + SCB / 2 - 1, a token and half of the blocks
   // a thread: requested by one step, put into their half of the buffer by the next
-  constexpr int SU = SCB / 4, SH = TN > 128 ? 2 : 1;
-  const int st = tid & 255, su = wave >> 2;
+  constexpr int SB = 512 / TT, SU = SCB / 2 / SB, SH = TN > 128 ? 2 : 1;
+  const int st = tid & (TT - 1), su = wave / (TT / 64);
   uint32_t sx[SU], sw[SU][SH];
   auto request_scales = [&](int b0) {
 #pragma unroll
     for (int u = 0; u < SU; ++u) {
-      const int at = min(first + b0 + su + 2 * u, kb - 1);
+      const int at = min(first + b0 + su + SB * u, kb - 1);
       sx[u] = g.sx[(t0 + min(st, ntok - 1)) * g.ldsx + at];
 #pragma unroll
       for (int h = 0; h < SH; ++h) {
@@ -284,9 +289,14 @@ MOE_DEV void fp8_tile(const Fp8Args &g, int tiles_n, int tiles_t, int splits, fl
     for (int u = 0; u < SU; ++u)
 #pragma unroll
       for (int h = 0; h < SH; ++h) {
+        float *const to = &l.s[(b0 + su + SB * u) % SCB][h][st / (TT / 2)][st & 15][(st >> 4) % NT];
+        if constexpr (ACC) {
+          *reinterpret_cast<uint32_t *>(to) = sx[u] | sw[u][h] << 8;
+          continue;
+        }
         // a byte is 2^(e - 127); 0 is the subnormal 2^-127, 255 is NaN
         const uint32_t e = sw[u][h], f = !E8 ? e : e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23;
-        l.s[(b0 + su + 2 * u) % SCB][h][st >> 7][st & 15][st >> 4 & 7] = e8m0_to_float(sx[u]) * __uint_as_float(f);
+        *to = e8m0_to_float(sx[u]) * __uint_as_float(f);
       }
   };
 
@@ -301,33 +311,38 @@ MOE_DEV void fp8_tile(const Fp8Args &g, int tiles_n, int tiles_t, int splits, fl
   for (int q = 0; q < 2; ++q) {
     const uint32_t at = 128 * r16 + 16 * ((kg + 4 * q) ^ sz);
     wa[q] = lds_addr(l.w[0]) + 2048 * MT * wn + at;
-    xa[q] = lds_addr(l.x[0]) + 16384 * wt + at;
+    xa[q] = lds_addr(l.x[0]) + 2048 * NT * wt + at;
   }
   const uint32_t sa = lds_addr(reinterpret_cast<const uint8_t *>(l.s[0][16 * MT * wn >= 128][wt][r16]));
+  constexpr int SBYTES = sizeof(l.s[0]);
 
-  static_for<WL + XL>([&](auto uc) { request(0, 0, uc); });
+  static_for<ST - 1>([&](auto sc) {
+    constexpr int s = decltype(sc)::value;
+    static_for<WL + XL>([&](auto uc) { request(s, s, uc); });
+  });
   request_scales(0);
   put_scales(0);
   auto step = [&](auto hc, int b) {
     constexpr int h = decltype(hc)::value;
-    // this block has landed, and every wave is done with the one before
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    __syncthreads();
+    // this block has landed (of three stages: what was requested since is the
+    // next), and every wave is done with the one before, whose stage is filled below
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm((WL + XL) * (ST - 2)));
+    __builtin_amdgcn_s_barrier();
     if (b % (SCB / 2) == 0) request_scales(b + SCB / 2);
     else if (b % (SCB / 2) == 1) put_scales(b - 1 + SCB / 2);  // whose half nobody reads any more
-    u32x4_t sc[2], w[MT][2], x[2][2];
+    u32x4_t sc[NT / 4], w[MT][2], x[2][2];
+    const uint32_t wh[2] = {wa[0] + h * TN * 128, wa[1] + h * TN * 128}, xh[2] = {xa[0] + h * TT * 128, xa[1] + h * TT * 128};
     auto read_x = [&](auto ic) {
       constexpr int i = decltype(ic)::value;
-      tread<h * TT * 128 + 2048 * i>(xa[0], x[i & 1][0]);
-      tread<h * TT * 128 + 2048 * i>(xa[1], x[i & 1][1]);
+      tread<2048 * i>(xh[0], x[i & 1][0]);
+      tread<2048 * i>(xh[1], x[i & 1][1]);
     };
-    tread<0>(sa + b % SCB * 2048, sc[0]);
-    tread<16>(sa + b % SCB * 2048, sc[1]);
+    static_for<NT / 4>([&](auto qc) { tread<16 * decltype(qc)::value>(sa + b % SCB * SBYTES, sc[decltype(qc)::value]); });
     read_x(std::integral_constant<int, 0>{});
     static_for<MT>([&](auto mc) {
       constexpr int m = decltype(mc)::value;
-      tread<h * TN * 128 + 2048 * m>(wa[0], w[m][0]);
-      tread<h * TN * 128 + 2048 * m>(wa[1], w[m][1]);
+      tread<2048 * m>(wh[0], w[m][0]);
+      tread<2048 * m>(wh[1], w[m][1]);
     });
     read_x(std::integral_constant<int, 1>{});
     f32x4_t p[2][MT];
@@ -349,32 +364,39 @@ MOE_DEV void fp8_tile(const Fp8Args &g, int tiles_n, int tiles_t, int splits, fl
         ttie(x[i & 1][0]);
         ttie(x[i & 1][1]);
       }
-      if constexpr (i < (WL + XL + 1) / 2) {
-        request(h ^ 1, b + 1, std::integral_constant<int, 2 * i>{});
-        request(h ^ 1, b + 1, std::integral_constant<int, 2 * i + 1>{});
-      }
+      // the loads into the free stage, spread over the products (of two stages:
+      // the first half, the rest is their time to land)
+      constexpr int over = ST == 2 ? NT / 2 : NT, per = (WL + XL + over - 1) / over;
+      if constexpr (i < over)
+        static_for<per>([&](auto uc) {
+          request((h + ST - 1) % ST, b + ST - 1, std::integral_constant<int, per * i + decltype(uc)::value>{});
+        });
       if constexpr (F8) {
         static_for<MT>([&](auto mc) {
           constexpr int m = decltype(mc)::value;
           if constexpr (i == 0) {  // the weights as they come
             twait<2 * (MT - 1 - m) + 2>();
             if constexpr (m == 0) {
-              ttie(sc[0]);
-              ttie(sc[1]);
+#pragma unroll
+              for (int q = 0; q < NT / 4; ++q) ttie(sc[q]);
               ttie(x[0][0]);
               ttie(x[0][1]);
             }
             ttie(w[m][0]);
             ttie(w[m][1]);
           }
-          p[i & 1][m] = mfma_f8(w[m], x[i & 1]);
-          if constexpr (i > 0) add(i - 1, m);
+          if constexpr (ACC) {
+            acc[m][i] = mfma_f8(w[m], x[i & 1], acc[m][i], sc[i >> 2][i & 3]);
+          } else {
+            p[i & 1][m] = mfma_f8(w[m], x[i & 1], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0x7F7Fu);
+            if constexpr (i > 0) add(i - 1, m);
+          }
         });
       } else {
         if constexpr (i == 0) {
           twait<2>();
-          ttie(sc[0]);
-          ttie(sc[1]);
+#pragma unroll
+          for (int q = 0; q < NT / 4; ++q) ttie(sc[q]);
           ttie(x[0][0]);
           ttie(x[0][1]);
 #pragma unroll
@@ -398,18 +420,20 @@ MOE_DEV void fp8_tile(const Fp8Args &g, int tiles_n, int tiles_t, int splits, fl
         }
       }
     });
+    if constexpr (!ACC) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) add(NT - 1, m);
+      for (int m = 0; m < MT; ++m) add(NT - 1, m);
+    }
   };
-  for (int b = 0; b < nblk; b += 2) {
-    step(std::integral_constant<int, 0>{}, b);
-    if (b + 1 < nblk) step(std::integral_constant<int, 1>{}, b + 1);
-  }
+  for (int b = 0; b < nblk; b += ST)
+    static_for<ST>([&](auto hc) {
+      if (b + decltype(hc)::value < nblk) step(hc, b + decltype(hc)::value);
+    });
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   const int nw = n0 + 16 * MT * wn, ldp = (g.N + 3) & ~3;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int t = 128 * wt + 16 * i + r16;
+    const int t = TT / 2 * wt + 16 * i + r16;
     if (t < ntok)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
@@ -420,11 +444,37 @@ MOE_DEV void fp8_tile(const Fp8Args &g, int tiles_n, int tiles_t, int splits, fl
   }
 }
 
-template <int MT, bool F8, bool E8, typename O>
-__global__ __launch_bounds__(512, 2) void fp8_tile_kernel(Fp8Args g, int tiles_n, int tiles_t, int splits,
-                                                          float *partial) {
-  __shared__ __attribute__((aligned(1024))) TileLds<MT> l;
-  fp8_tile<MT, F8, E8, O>(g, tiles_n, tiles_t, splits, partial, l);
+// block -> tile of `total`, as xcd_logical
+MOE_DEV int tile_of(int block, int total) {
+  const int t8 = (total + 7) & ~7, id = (block & 7) * (t8 >> 3) + (block >> 3);
+  return block < t8 && id < total ? id : -1;
+}
+
+// fp32 out: tiles of 128 rows and 256 tokens
+template <bool E8>
+__global__ __launch_bounds__(512, 2) void fp8_tile_f32_kernel(Fp8Args g, int splits, float *partial) {
+  __shared__ __attribute__((aligned(1024))) TileLds<2, 8, 2> l;
+  const int tn = (g.N + 127) / 128, tt = (g.T + 255) / 256, work = tile_of(blockIdx.x, tn * tt * splits);
+  if (work >= 0) fp8_tile<2, 8, 2, false, E8, float>(g, work, 0, tn, tt, splits, partial, l);
+}
+
+// bf16 out: tiles of 256 rows and 256 tokens for the first rows, of 256 rows and
+// 128 tokens for the others; K is split where there are none of the first kind
+template <bool E8>
+__global__ __launch_bounds__(512, 2) void fp8_tile_bf16_kernel(Fp8Args g, int rows, int splits, float *partial) {
+  __shared__ __attribute__((aligned(1024))) union L {
+    TileLds<4, 8, 2> big;
+    TileLds<4, 4, 3> small;
+    __device__ L() {}
+  } l;
+  const int tn = rows / 256, tt = (g.T + 255) / 256, big = (tn * tt + 7) & ~7;
+  if ((int)blockIdx.x < big) {
+    const int work = tile_of(blockIdx.x, tn * tt);
+    if (work >= 0) fp8_tile<4, 8, 2, true, E8, uint16_t>(g, work, 0, tn, tt, 1, partial, l.big);
+    return;
+  }
+  const int sn = max(g.N - rows + 255, 0) / 256, st = (g.T + 127) / 128, work = tile_of(blockIdx.x - big, sn * st * splits);
+  if (work >= 0) fp8_tile<4, 4, 3, true, E8, uint16_t>(g, work, rows, sn, st, splits, partial, l.small);
 }
 
 // the splits' sums in order, four columns a thread
@@ -453,44 +503,49 @@ void stream_by_type(const Fp8Args &g, bool e8, bool out_bf16, hipStream_t st) {
   }
 }
 
-template <int MT, bool F8, typename O>
-void tile_by_type(const Fp8Args &g, bool e8, int splits, float *partial, hipStream_t st) {
-  const int tn = (g.N + 64 * MT - 1) / (64 * MT), tt = (g.T + 255) / 256;
-  const dim3 gr((unsigned)((tn * tt * splits + 7) / 8 * 8)), blk(512);
-  if (e8) hipLaunchKernelGGL((fp8_tile_kernel<MT, F8, true, O>), gr, blk, 0, st, g, tn, tt, splits, partial);
-  else hipLaunchKernelGGL((fp8_tile_kernel<MT, F8, false, O>), gr, blk, 0, st, g, tn, tt, splits, partial);
-  if (splits > 1)
-    hipLaunchKernelGGL(fp8_join_kernel<O>, dim3((unsigned)(((long long)g.T * ((g.N + 3) / 4) + 255) / 256)), dim3(256),
-                       0, st, g, splits, partial);
-}
-
 }  // namespace
 
-// How the tile kernel splits K: where the tiles are fewer than the CUs, into
-// about one work-group a CU, of four blocks at least; and what the product then
-// takes, in us: 10 for the kernel's ends, 1.1 + rows / 400 for a block, and the
-// parts' sums written and read at 4 TB/s.
+// How the tile kernels cut a product, and what it then takes, in us: 8 for the
+// ends of a kernel; of a turn (256 tiles, one a CU) 1.75 a block for tiles of
+// 256 x 256, 1.15 for 256 rows x 128 tokens, 1.45 for 128 x 256 with fp32 sums.
+// The first kind reads least per product, the second fills turns better:
+// 4096 tokens and 6144 rows are 384 of the first (half of the second turn
+// empty, 208 us), 768 of the second (three turns, 210), or 256 of the first and
+// then 256 of the second (193).  Where the tiles are fewer than the CUs, K is
+// split into about one work-group a CU, of four blocks at least, and the parts'
+// sums are written and read at 3 TB/s.
 struct TilePlan {
+  int rows;  // bf16 out: rows in tiles of the first kind
   int splits;
   double us;
 };
 static TilePlan tile_plan(int T, int N, int K, bool out_bf16) {
-  const int rows = out_bf16 ? 256 : 128;
-  const long long tiles = (long long)((N + rows - 1) / rows) * ((T + 255) / 256);
-  const int kb = (K + 127) / 128;
-  const int s = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(256 / tiles, kb / 4), 16));
-  const double rounds = (double)((tiles * s + 255) / 256);
-  return {s, 10 + (1.1 + rows / 400.0) * ((kb + s - 1) / s) * rounds + (s > 1 ? 2e-6 * s * T * N : 0.0)};
+  const long long kb = (K + 127) / 128, CUS = 256;
+  auto up = [](long long a, long long b) { return (a + b - 1) / b; };
+  const long long small = out_bf16 ? up(N, 256) * up(T, 128) : up(N, 128) * up(T, 256);
+  const double step = out_bf16 ? 1.15 : 1.45;
+  const long long s = std::max(1LL, std::min(std::min(CUS / small, kb / 4), 16LL));
+  TilePlan best{0, (int)s, 8 + step * (double)(up(kb, s) * up(small * s, CUS)) + (s > 1 ? 2.6e-6 * s * T * N : 0.0)};
+  if (!out_bf16 || s > 1) return best;
+  // whole turns of the first kind, or all of it
+  const long long tn = up(N, 256), tt = up(T, 256);
+  for (long long turns = 1; turns <= up(tn * tt, CUS); ++turns) {
+    const long long n = std::min(tn, turns * CUS / tt);
+    if (n == 0) continue;
+    const double us = 8 + (double)kb * (1.75 * (double)up(n * tt, CUS) + step * (double)up((tn - n) * up(T, 128), CUS));
+    if (us < best.us) best = {(int)(256 * n), 1, us};
+  }
+  return best;
 }
 // Whether the stream kernel is faster: its work-groups of 32 rows and 64 tokens
-// take 0.43 us a block, one a CU at a time.  Measured at K = 7168, bf16 out,
+// take 0.38 us a block, one a CU at a time.  Measured at K = 7168, bf16 out,
 // stream against tiles: 64 tokens and 6144 rows 24 / 22 us, 512 and 895 24 / 29,
 // 128 and 6144 48 / 28, 1024 and 895 46 / 30, 512 and 6144 135 / 47; at K = 512,
 // 300 tokens and 3584 rows, 11 / 17.  Up to 64 tokens it is always taken.
 static bool stream_fits(const TilePlan &tile, int T, int N, int K) {
   if (T <= 64) return true;
   const long long groups = (long long)((N + 31) / 32) * ((T + 63) / 64);
-  return 3 + 0.43 * ((K + 127) / 128) * (double)((groups + 255) / 256) <= tile.us;
+  return 2.5 + 0.38 * ((K + 127) / 128) * (double)((groups + 255) / 256) <= tile.us;
 }
 
 size_t fp8_workspace_bytes(int T, int N, int K) {
@@ -506,8 +561,23 @@ hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, h
   const TilePlan p = tile_plan(g.T, g.N, g.K, out_bf16);
   if (!stream_fits(p, g.T, g.N, g.K)) {
     float *partial = static_cast<float *>(ws);
-    if (out_bf16) tile_by_type<4, true, uint16_t>(g, e8, p.splits, partial, st);
-    else tile_by_type<2, false, float>(g, e8, p.splits, partial, st);
+    auto up8 = [](int v) { return (unsigned)((v + 7) & ~7); };
+    const dim3 blk(512);
+    if (out_bf16) {
+      const int rest = std::max(g.N - p.rows, 0);
+      const dim3 gr(up8(p.rows / 256 * ((g.T + 255) / 256)) + up8((rest + 255) / 256 * ((g.T + 127) / 128) * p.splits));
+      if (e8) hipLaunchKernelGGL(fp8_tile_bf16_kernel<true>, gr, blk, 0, st, g, p.rows, p.splits, partial);
+      else hipLaunchKernelGGL(fp8_tile_bf16_kernel<false>, gr, blk, 0, st, g, p.rows, p.splits, partial);
+    } else {
+      const dim3 gr(up8((g.N + 127) / 128 * ((g.T + 255) / 256) * p.splits));
+      if (e8) hipLaunchKernelGGL(fp8_tile_f32_kernel<true>, gr, blk, 0, st, g, p.splits, partial);
+      else hipLaunchKernelGGL(fp8_tile_f32_kernel<false>, gr, blk, 0, st, g, p.splits, partial);
+    }
+    if (p.splits > 1) {
+      const dim3 jr((unsigned)(((long long)g.T * ((g.N + 3) / 4) + 255) / 256));
+      if (out_bf16) hipLaunchKernelGGL(fp8_join_kernel<uint16_t>, jr, dim3(256), 0, st, g, p.splits, partial);
+      else hipLaunchKernelGGL(fp8_join_kernel<float>, jr, dim3(256), 0, st, g, p.splits, partial);
+    }
   } else if (g.T <= 16) {
     stream_by_type<1, 1, 8, 4>(g, e8, out_bf16, st);
   } else if (g.T <= 32) {

@@ -168,15 +168,20 @@ def _enqueue(name, device, stream, *args):
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors must be on a GPU, not {device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        # the handle of torch.cuda.current_stream(device), without the 1.8 us of making that object
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on {device}")
+    else:
+        handle = stream.cuda_stream
     fn = getattr(load(), name)
     if torch.cuda.current_device() == device.index:
-        check(name, fn(*args, stream.cuda_stream))
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            check(name, fn(*args, stream.cuda_stream))
+            rc = fn(*args, handle)
+    if rc:
+        check(name, rc)
 
 
 def block_pre_norm(x, gamma, eps=1e-6, n=None, q=None, q_scale=None, stream=None):
@@ -354,7 +359,6 @@ class LatentMoE:
         self.device = torch.device(device)
         self._bufs: dict = {}
         self._few_bufs: dict = {}
-        self._few_weights = None
         self.overlap_shared = overlap_shared
         # at decode sizes the latent projection z joins the shared experts on
         # the side stream, so the main stream's routing is only the router and
@@ -509,8 +513,6 @@ class LatentMoE:
         dev = self.w["w_router"].device
         if x.dtype != torch.bfloat16 or not x.is_contiguous() or x.device != dev:
             raise ValueError(f"forward_few: x must be contiguous bfloat16 on {dev}")
-        if self._few_weights is None:
-            self._few_weights = layer_weights(self.w)
         b = self._few_bufs.get(T)
         if b is None:
             s = self.shape
@@ -520,5 +522,5 @@ class LatentMoE:
                 "out": torch.empty((T, s.hidden), dtype=torch.float32, device=dev),
                 "ws": torch.empty((max(16, layer_few_workspace_bytes(s, T)),), dtype=torch.uint8, device=dev),
             }
-        layer_few(self.shape, x, self._few_weights, b["topk_ids"], b["topk_w"], b["out"], b["ws"], stream)
+        layer_few(self.shape, x, layer_weights(self.w), b["topk_ids"], b["topk_w"], b["out"], b["ws"], stream)
         return b

@@ -120,6 +120,85 @@ def test_exact_sums(mx, T, N, K, kind):
         assert torch.equal(out.cpu(), want)
 
 
+# K in parts; tiles of 128 tokens in one turn; of 256 in one turn; first of 256, then of 128; long K
+TILES = [(130, 3000, 4112), (1500, 3000, 272), (3000, 3000, 144), (4100, 4500, 272), (100, 6144, 7168)]
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("T,N,K", TILES)
+def test_tiles(mx, T, N, K, kind, out):
+    say(f"case: 8-bit product by tiles T={T} N={N} K={K} scales {kind} out {out}")
+    run(mx, T, N, K, kind, out, seed=T + K, pad=16, opad=4 if N < 4000 else 1)
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("T,N,K", TILES[:4])
+def test_tiles_exact_and_nan(mx, T, N, K, kind):
+    """As test_exact_sums, in both outputs; then one NaN code in each operand, which stays in its row and column."""
+    say(f"case: 8-bit product by tiles, exact sums, T={T} N={N} K={K} scales {kind}")
+    rng = np.random.default_rng(N)
+    kb, nb = -(-K // 128), -(-N // 128)
+    x, w = ((0x38 + rng.integers(0, 8, s) + 0x80 * rng.integers(0, 2, s)).astype(np.uint8) for s in ((T, K), (N, K)))
+    xs = rng.integers(125, 130, (T, kb)).astype(np.uint8)
+    e = rng.integers(125, 130, (nb, kb))
+    ws = e.astype(np.uint8) if kind == "e8m0" else (2.0 ** (e - 127.0)).astype(np.float32)
+    d = [torch.from_numpy(v).to(DEV) for v in (x, xs, w, ws)]
+    scratch = torch.empty(mx.fp8_gemm_workspace_bytes(T, N, K), dtype=torch.uint8, device=DEV)
+    a = e4m3(x).astype(np.float32) * np.repeat(2.0 ** (xs.astype(np.float32) - 127), 128, 1)[:, :K]
+    b = e4m3(w).astype(np.float32) * np.repeat(np.repeat(2.0 ** (e - 127.0), 128, 0)[:N], 128, 1)[:, :K].astype(np.float32)
+    want = torch.from_numpy(a @ b.T)  # sums of under 2^24 steps of 2^-10: exact in fp32 in any order
+    bad = torch.zeros((T, N), dtype=torch.bool, device=DEV)
+    bad[T - 2] = True
+    bad[:, N - 1] = True
+    for dt in (torch.float32, torch.bfloat16):
+        d[0][T - 2, K - 1], d[2][N - 1, 0] = int(x[T - 2, K - 1]), int(w[N - 1, 0])
+        out = torch.empty((T, N), dtype=dt, device=DEV)
+        mx.fp8_gemm(*d, out, scratch)
+        assert torch.equal(out.cpu(), want.to(dt))
+        d[0][T - 2, K - 1], d[2][N - 1, 0] = 0x7F, 0xFF
+        got = torch.empty((T, N), dtype=dt, device=DEV)
+        mx.fp8_gemm(*d, got, scratch)
+        assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], out[~bad])
+
+
+def test_tiles_on_streams_and_replayed(mx):
+    """K in parts: the parts' sums in a workspace of the call's own."""
+    T, N, K = 130, 3000, 4112
+    say("case: 8-bit product by tiles on two streams and replayed")
+    nb = mx.fp8_gemm_workspace_bytes(T, N, K)
+    assert nb > T * N * 8
+    ops, want, out, scratch = [], [], [], []
+    for seed in (1, 2):
+        x, xs, w, ws = operands(T, N, K, "f32", seed)
+        ops.append([torch.from_numpy(v.copy()).to(DEV) for v in (x, xs[:, :-1], w, ws)])
+        scratch.append(torch.empty(nb, dtype=torch.uint8, device=DEV))
+        want.append(torch.empty((T, N), dtype=torch.bfloat16, device=DEV))
+        out.append(torch.empty((T, N), dtype=torch.bfloat16, device=DEV))
+        mx.fp8_gemm(*ops[-1], want[-1], scratch[-1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i in range(2):
+            mx.fp8_gemm(*ops[i], out[i], scratch[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want))
+    # two graphs that share a workspace, one after the other, with eager calls between
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            mx.fp8_gemm(*ops[i], out[i], scratch[0])
+        graphs.append(g)
+    for _ in range(3):
+        for i in range(2):
+            out[i].zero_()
+            graphs[i].replay()
+            mx.fp8_gemm(*ops[1], want[1], scratch[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 @pytest.mark.parametrize("T,N,K", [(3, 100, 400), (40, 129, 272), (200, 200, 512), (520, 384, 1152)])
 def test_strides_and_accumulate(mx, T, N, K):
     for opad in (1, 4):

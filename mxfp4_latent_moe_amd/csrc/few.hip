@@ -198,7 +198,7 @@ MOE_DEV void topk_group(const FewArgs &a, TopkLds &l) {
       key[i] = lane + 64 * i < a.E ? order_key(b) : 0u;
     }
     uint32_t th, kp1;
-    select_topk(key, sg, a.k, lane, l.sel[t], l.s[t], l.kl[t], th, kp1);
+    select_topk<false>(key, sg, a.k, lane, l.sel[t], l.s[t], l.kl[t], th, kp1);
   }
   __syncthreads();
   if (t < a.T && lane < a.k) {

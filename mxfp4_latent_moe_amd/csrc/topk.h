@@ -29,6 +29,9 @@ MOE_DEV int lanes_below(uint64_t m) {
 // The k-th largest key of a wavefront's SLOTS x 64 keys and the selection
 // (see above): the selected ids, scores and keys go to sel / s / kl in
 // ascending id order; th is the k-th largest key, kp1 the (k+1)-th.
+// GAP false: the search ends as soon as a candidate has exactly k keys at or
+// above it; th is then that candidate and kp1 the largest key below it.
+template <bool GAP = true>
 MOE_DEV void select_topk(const uint32_t (&key)[SLOTS], const float (&sg)[SLOTS], int k, int lane, int *sel,
                          float *s, uint32_t *kl, uint32_t &th_out, uint32_t &kp1_out) {
   auto count_ge = [&](uint32_t c) {
@@ -40,7 +43,10 @@ MOE_DEV void select_topk(const uint32_t (&key)[SLOTS], const float (&sg)[SLOTS],
   uint32_t th = 0u;  // the largest c with at least k keys >= c: the k-th largest key
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t c = th | (1u << bit);
-    if (count_ge(c) >= k) th = c;
+    const int n = count_ge(c);
+    if (n >= k) th = c;
+    if constexpr (!GAP)
+      if (n == k) break;
   }
   int above = 0, at_or_above = 0;
 #pragma unroll

@@ -322,6 +322,7 @@ MOE_DEV void fp8_tile(const Fp8Args &g, int work, int row0, int tiles_n, int til
   });
   request_scales(0);
   put_scales(0);
+  twait<0>();  // in LDS before the first barrier (later ones are, by the reads' own waits behind them)
   auto step = [&](auto hc, int b) {
     constexpr int h = decltype(hc)::value;
     // this block has landed (of three stages: what was requested since is the

@@ -162,6 +162,13 @@ def test_tiles_exact_and_nan(mx, T, N, K, kind):
         assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], out[~bad])
 
 
+@pytest.mark.parametrize("T,N,K", [TILES[0], TILES[1], (100, 3002, 7168)])
+def test_tiles_accumulate(mx, T, N, K):
+    for opad in (1, 4):
+        say(f"case: 8-bit product by tiles, added to: T={T} N={N} K={K} out pad {opad}")
+        run(mx, T, N, K, "f32", "f32", seed=1, pad=16, opad=opad, accumulate=True)
+
+
 def test_tiles_on_streams_and_replayed(mx):
     """K in parts: the parts' sums in a workspace of the call's own."""
     T, N, K = 130, 3000, 4112

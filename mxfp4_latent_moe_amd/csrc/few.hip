@@ -32,6 +32,7 @@
 // Requests further ahead are no faster: two groups of K steps ahead in the
 // expert products 50 against 46 us at one token (one work-group a CU fits), and
 // in the bf16 products four steps a round 58 against 38.
+#include <algorithm>
 #include <atomic>
 
 #include "kernels.h"
@@ -541,8 +542,8 @@ hipError_t launch_few(const FewArgs &a, hipStream_t st) {
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(few_shared_kernel, dim3((unsigned)(1 + a.S / 8)), dim3(FTHR), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  // two work-groups a CU where their columns fit
-  auto groups = [&](size_t lds) { return ncu * (lds <= 80 * 1024 ? 2 : 1); };
+  // two work-groups a CU where their columns fit, and no more than there can be items
+  auto groups = [&](size_t lds, int N) { return std::min(ncu * (lds <= 80 * 1024 ? 2 : 1), a.T * a.k * (N / ROWS)); };
   const size_t l1 = columns_bytes(a.T, a.L), l2 = columns_bytes(a.T, a.I);
   if (l1 > 64 * 1024)
     if ((e = hipFuncSetAttribute(reinterpret_cast<const void *>(&few_expert_kernel<true>),
@@ -552,10 +553,10 @@ hipError_t launch_few(const FewArgs &a, hipStream_t st) {
     if ((e = hipFuncSetAttribute(reinterpret_cast<const void *>(&few_expert_kernel<false>),
                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)l2)) != hipSuccess)
       return e;
-  hipLaunchKernelGGL(few_expert_kernel<true>, dim3((unsigned)groups(l1)), dim3(FTHR), l1, st, a, groups(l1));
+  const int g1 = groups(l1, a.I), g2 = groups(l2, a.L);
+  hipLaunchKernelGGL(few_expert_kernel<true>, dim3((unsigned)g1), dim3(FTHR), l1, st, a, g1);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(few_expert_kernel<false>, dim3((unsigned)(groups(l2) + a.H / 16 * (a.S > 0))), dim3(FTHR), l2, st, a,
-                     groups(l2));
+  hipLaunchKernelGGL(few_expert_kernel<false>, dim3((unsigned)(g2 + a.H / 16 * (a.S > 0))), dim3(FTHR), l2, st, a, g2);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int nb = (a.L + CMB - 1) / CMB;
   hipLaunchKernelGGL(few_combine_kernel, dim3((unsigned)nb, (unsigned)a.T), dim3(64), 0, st, a);

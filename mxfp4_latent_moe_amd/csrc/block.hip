@@ -127,14 +127,8 @@ MOE_DEV void write_normed(const NormOut &o, long long t, int H, bool vec, const 
     if (o.n != nullptr) store8<uint16_t>(o.n + t * o.ldn, c, H, vec, n);
     if (o.q != nullptr) {
       // a block of 128 channels is 16 neighbouring lanes; lanes past the row hold zeros
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(n[i]));
-#pragma unroll
-      for (int d = 8; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
-      const uint32_t sb = q8_scale_byte(amax);
-      const float inv = q8_inverse(sb);
-      const uint32_t lo = q8_pack4(n[0], n[1], n[2], n[3], inv), hi = q8_pack4(n[4], n[5], n[6], n[7], inv);
+      uint32_t lo, hi;
+      const uint32_t sb = q8_block(n, lo, hi);
       uint8_t *q = o.q + t * o.ldq;
       if (vec) {
         if (c < H) *reinterpret_cast<u32x2_t *>(q + c) = u32x2_t{lo, hi};
@@ -208,28 +202,22 @@ __global__ __launch_bounds__(NT) void post_norm_kernel(PostNormArgs a) {
 }
 
 // e4m3 codes and scales of rows of fp32 or bf16 values: a block of 128 is 16
-// lanes of 8 values, one pass, bound by memory
+// lanes of 8 values, one pass, bound by memory: 4096 rows of 7168 bf16 20.8 us
+// (88 MB, 4.2 TB/s).  Two and four blocks a thread took 2% and 16% longer.
 template <typename X>
 __global__ __launch_bounds__(256) void quantize8_kernel(const X *__restrict__ x, long long ldx, long long T, int K,
                                                         int vec, uint8_t *__restrict__ q, long long ldq,
                                                         uint8_t *__restrict__ qs, long long ldqs) {
   const int kb = (K + Q8_BLOCK - 1) / Q8_BLOCK;
-  const long long blk = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const long long t = blk / kb;
-  const int b = (int)(blk - t * kb);
-  const bool live = t < T;
+  const long long first = 16LL * blockIdx.x, t0 = first / kb;  // of the work-group
+  const int b0 = (int)(first - t0 * kb) + (threadIdx.x >> 4), r = b0 / kb, b = b0 - r * kb;
+  const long long t = t0 + r;
   const int c = b * Q8_BLOCK + 8 * (threadIdx.x & 15);
   f32x8_t v{};
-  if (live) v = load8<X>(x + t * ldx, c, K, vec);
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(v[i]));
-#pragma unroll
-  for (int d = 8; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
-  if (!live) return;
-  const uint32_t sb = q8_scale_byte(amax);
-  const float inv = q8_inverse(sb);
-  const uint32_t lo = q8_pack4(v[0], v[1], v[2], v[3], inv), hi = q8_pack4(v[4], v[5], v[6], v[7], inv);
+  if (t < T) v = load8<X>(x + t * ldx, c, K, vec);
+  uint32_t lo, hi;
+  const uint32_t sb = q8_block(v, lo, hi);
+  if (t >= T) return;
   uint8_t *row = q + t * ldq;
   if (vec) {
     if (c < K) *reinterpret_cast<u32x2_t *>(row + c) = u32x2_t{lo, hi};

@@ -1,7 +1,9 @@
 """Torch-facing wrappers of the C-ABI calls (the five of the layer, the capped
-routing, the REAP saliency and the combine with REAP fused in), and a layer object that chains the layer's calls on one stream.  Argument marshalling only: tensors are passed as
-device pointers, the stream as its HIP handle; all compute runs in the HIP
-library."""
+routing, the REAP saliency and the combine with REAP fused in; the norms around
+the block, the 8-bit product and the layer for a few tokens), and a layer object
+that chains the layer's calls on one stream.  Argument marshalling only: tensors
+are passed as device pointers, the stream as its HIP handle; all compute runs in
+the HIP library."""
 from __future__ import annotations
 
 import ctypes

@@ -248,6 +248,33 @@ def test_nan_stays_in_its_row_and_column(mx):
         assert torch.isnan(out[bad]).all() and torch.equal(out[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("T,N,K", [(5, 900, 400), (60, 900, 400), TILES[0], TILES[1], TILES[3]])
+def test_scale_bytes_at_their_ends(mx, T, N, K):
+    """Weight scale bytes 255 (NaN) and 0 (2^-127), activation bytes 1 and 247: NaN in the block's rows, nothing
+    elsewhere; the small and the large values as the formula has them."""
+    say(f"case: 8-bit product, scale bytes at their ends, T={T} N={N} K={K}")
+    x, xs, w, ws = operands(T, N, K, "e8m0", 4)
+    xs = xs[:, :-1].copy()
+    xs[1], xs[3] = 247, 1
+    ws[2, 0], ws[5] = 255, 0
+    d = [torch.from_numpy(v).to(DEV) for v in (x, xs, w, ws)]
+    scratch = torch.empty(mx.fp8_gemm_workspace_bytes(T, N, K), dtype=torch.uint8, device=DEV)
+    bad = np.zeros(N, bool)
+    bad[256:384] = True
+    ts = np.unique([0, 1, 2, 3, 4, T - 1])
+    ws[2, 0] = 120
+    ref, mag, top = reference(x[ts], xs[ts], w, ws, K, "e8m0")
+    for out_kind, dt in (("f32", torch.float32), ("bf16", torch.bfloat16)):
+        out = torch.empty((T, N), dtype=dt, device=DEV)
+        mx.fp8_gemm(*d, out, scratch)
+        got = out.float().cpu().numpy().astype(np.float64)
+        assert np.isnan(got[:, bad]).all() and not np.isnan(np.delete(got, 1, 0)[:, ~bad]).any()
+        # token 1's sums of magnitudes pass 2^128: its partial sums may be infinite, and their sum NaN
+        with np.errstate(all="ignore"):
+            ok = (np.abs(got[ts] - ref) <= bound(mag, top, K, out_kind, ref)) | (mag >= 2.0 ** 127)
+        assert ok[:, ~bad].all() and (mag < 2.0 ** 127)[ts != 1][:, ~bad].all()
+
+
 def test_quantize_then_product(mx):
     """As used: bf16 rows, quantised, then the product, against the bf16 rows' own product in fp64 with the
     rounding of each operand value (2^-4, or half the grid's smallest step) counted."""

@@ -47,7 +47,7 @@ constexpr int SU = 3;            // K steps a round of the shared gate/up
 constexpr int CMB = 256;         // columns of a combine work-group
 constexpr int AHEAD = 1;         // groups of K steps requested ahead, of
 constexpr int D = 4;             // K steps (128 values) each
-constexpr int ROWS = 16 * FNW;   // weight rows of an expert item
+constexpr int ROWS = 16 * FNW;   // weight rows of an expert item whose waves split the rows
 
 MOE_DEV int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -304,13 +304,19 @@ __global__ __launch_bounds__(FTHR, 4) void few_shared_kernel(FewArgs a) {
 // list entry; a work-group has a contiguous range of the items.  Each wave
 // streams its rows over the whole of K, four K steps (256 contiguous bytes a
 // row) a group, one group ahead, across items; the entry's columns sit in LDS
-// and are staged when the entry changes.
-template <bool PAIR>
-MOE_DEV void expert_items(const FewArgs &a, u32x4_t *lds, int group, int groups) {
+// and are staged when the entry changes.  KSPLIT: an item is 16 rows, the waves
+// take the groups of K by turns and their sums are added in wave order: where
+// there are few items, a wave's groups one after the other are what takes time
+// (two experts of 256 x 3328: gate/up 8.8 us, 20.2 without).
+template <bool PAIR, bool KSPLIT>
+MOE_DEV void expert_items(const FewArgs &a, u32x4_t *lds, f32x4_t (*part)[2][64], int group, int groups) {
+  constexpr int IROWS = KSPLIT ? 16 : ROWS, KS = KSPLIT ? FNW : 1;
   constexpr int NM = PAIR ? 2 : 1;
   const int wave = uni(threadIdx.x >> 6), lane = lane_id(), kg = lane >> 4, r16 = lane & 15;
   const int N = PAIR ? a.I : a.L, K = PAIR ? a.L : a.I;
-  const int nks = K / 128, ng = (nks + D - 1) / D, nb = N / ROWS;
+  const int nks = K / 128, ng = (nks + D - 1) / D, nb = N / IROWS;
+  const int wrow = KSPLIT ? 0 : 16 * wave, ks = KSPLIT ? wave : 0;  // the wave's rows of an item, its first group
+  const int ngw = (ng + KS - 1) / KS;
   const int nc = 3 * min(a.T, FEW_ROWS);
   const uint32_t row_bytes = K / 2, srow_bytes = K / 32;
   // read through the constant address space: the scalar unit's reads stay off
@@ -334,7 +340,7 @@ MOE_DEV void expert_items(const FewArgs &a, u32x4_t *lds, int group, int groups)
       wr[m] = make_rsrc((PAIR ? (m ? a.w3 : a.w1) : a.w2) + e * N * row_bytes, (uint32_t)N * row_bytes);
       sr[m] = make_rsrc((PAIR ? (m ? a.s3 : a.s1) : a.s2) + e * N * srow_bytes, (uint32_t)N * srow_bytes);
     }
-    const uint32_t n = (it - c * nb) * ROWS + wave * 16 + r16;
+    const uint32_t n = (it - c * nb) * IROWS + wrow + r16;
     wo = n * row_bytes + kg * 16;
     so = n * srow_bytes;
   };
@@ -345,14 +351,14 @@ MOE_DEV void expert_items(const FewArgs &a, u32x4_t *lds, int group, int groups)
   // on into the next row (codes are finite; their columns are zeros).
   auto load_group = [&](int bi) {
     const bool live = l_item < i_end;
-    const uint32_t w0 = live ? wo : 0u, s0 = live ? so : 0u, q0 = live ? l_g * D : 0u;
+    const uint32_t w0 = live ? wo : 0u, s0 = live ? so : 0u, q0 = live ? min(ks + KS * l_g, ng - 1) * D : 0u;
 #pragma unroll
     for (int d = 0; d < D; ++d)
 #pragma unroll
       for (int m = 0; m < NM; ++m) wq[bi][d][m] = buf_load16(wr[m], w0, (q0 + d) * 64u);
 #pragma unroll
     for (int m = 0; m < NM; ++m) sq[bi][m] = buf_load16(sr[m], s0, q0 * 4u);
-    if (++l_g == ng) {
+    if (++l_g == ngw) {
       l_g = 0;
       if (++l_item < i_end) set_load_item(l_item);
     }
@@ -403,7 +409,23 @@ MOE_DEV void expert_items(const FewArgs &a, u32x4_t *lds, int group, int groups)
 #pragma unroll
   for (int m = 0; m < NM; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   auto finish = [&]() {
-    const int n0 = (item - c * nb) * ROWS + wave * 16 + 4 * kg, j = r16 / 3;
+    if constexpr (KSPLIT) {
+      __syncthreads();  // the sums of the item before have been read
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        part[wave][m][lane] = acc[m];
+        acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      __syncthreads();
+      if (wave != 0) return;
+#pragma unroll
+      for (int m = 0; m < NM; ++m) {
+        acc[m] = part[0][m][lane];
+#pragma unroll
+        for (int q = 1; q < FNW; ++q) acc[m] += part[q][m][lane];
+      }
+    }
+    const int n0 = (item - c * nb) * IROWS + wrow + 4 * kg, j = r16 / 3;
     f32x4_t v = plane_sum(acc[0]);
     if constexpr (PAIR) {
       const f32x4_t u = plane_sum(acc[NM - 1]);
@@ -420,25 +442,28 @@ MOE_DEV void expert_items(const FewArgs &a, u32x4_t *lds, int group, int groups)
   };
   // the groups of the work-group's items, a ring's turn an iteration; groups
   // past the last one are multiplied and dropped
-  for (int left = (i_end - i_begin) * ng; left > 0; left -= AHEAD + 1) {
+  for (int left = (i_end - i_begin) * ngw; left > 0; left -= AHEAD + 1) {
 #pragma unroll
     for (int b = 0; b <= AHEAD; ++b) {
       load_group((b + AHEAD) % (AHEAD + 1));
       __builtin_amdgcn_sched_barrier(0);
+      const int gg = ks + KS * g;
+      if (!KSPLIT || gg < ng) {
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        float sc[NM];
+        for (int d = 0; d < D; ++d) {
+          float sc[NM];
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
-          sc[m] = g * D + d < nks ? e8m0_to_float((sq[b][m][d] >> (8 * kg)) & 0xFFu) : 1.0f;
+          for (int m = 0; m < NM; ++m)
+            sc[m] = gg * D + d < nks ? e8m0_to_float((sq[b][m][d] >> (8 * kg)) & 0xFFu) : 1.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8_t x = __builtin_bit_cast(bf16x8_t, col[(16 * (g * D + d) + j) * nc]);
+          for (int j = 0; j < 4; ++j) {
+            const bf16x8_t x = __builtin_bit_cast(bf16x8_t, col[(16 * (gg * D + d) + j) * nc]);
 #pragma unroll
-          for (int m = 0; m < NM; ++m) acc[m] = mfma_16x16x32(fp4x8_to_bf16(wq[b][d][m][j], sc[m]), x, acc[m]);
+            for (int m = 0; m < NM; ++m) acc[m] = mfma_16x16x32(fp4x8_to_bf16(wq[b][d][m][j], sc[m]), x, acc[m]);
+          }
         }
       }
-      if (++g == ng) {
+      if (++g == ngw) {
         g = 0;
         if (item < i_end) {
           finish();
@@ -453,11 +478,12 @@ MOE_DEV void expert_items(const FewArgs &a, u32x4_t *lds, int group, int groups)
 }
 
 // gate/up; down with the shared experts' down products behind it
-template <bool PAIR>
+template <bool PAIR, bool KSPLIT>
 __global__ __launch_bounds__(FTHR, 2) void few_expert_kernel(FewArgs a, int groups) {
   extern __shared__ u32x4_t lds[];
+  __shared__ f32x4_t part[KSPLIT ? FNW : 1][2][64];
   if ((int)blockIdx.x < groups) {
-    expert_items<PAIR>(a, lds, blockIdx.x, groups);
+    expert_items<PAIR, KSPLIT>(a, lds, part, blockIdx.x, groups);
     return;
   }
   if constexpr (!PAIR) {
@@ -526,6 +552,29 @@ static size_t columns_bytes(int T, int K) {
   return b > FNW * 64 * 16 ? b : FNW * 64 * 16;
 }
 
+// An expert kernel: K split over the waves where the items of 128 rows are fewer
+// than half of the CUs, by a rule without T, so that a token's result does not
+// depend on its company; K is long; and there is room for the sums.  Measured
+// with / without: gate/up of K = 3328 8.8 / 20.2 us, 2944 12.8 / 20.4, 2048 8.5 /
+// 15.5; down (one matrix a wave) of 1792 8.9 / 8.2, of 256 6.1 / 5.4.  Two
+// work-groups a CU where their columns fit, and no more than there can be items;
+// `more` follow.
+template <bool PAIR>
+static hipError_t launch_expert(const FewArgs &a, int ncu, int N, int K, int more, hipStream_t st) {
+  const size_t lds = columns_bytes(a.T, K);
+  const int items = a.k * (N / ROWS);  // of a token
+  const bool split = FEW_MAX_T * items < ncu / 2 && K >= (PAIR ? 2048 : 2560) && columns_bytes(FEW_MAX_T, K) <= 128 * 1024;
+  const int groups = std::min(ncu * (lds <= 60 * 1024 ? 2 : 1), a.T * items * (split ? FNW : 1));
+  auto *fn = split ? &few_expert_kernel<PAIR, true> : &few_expert_kernel<PAIR, false>;
+  if (lds > 60 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(fn, dim3((unsigned)(groups + more)), dim3(FTHR), lds, st, a, groups);
+  return hipGetLastError();
+}
+
 hipError_t launch_few(const FewArgs &a, hipStream_t st) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -542,22 +591,8 @@ hipError_t launch_few(const FewArgs &a, hipStream_t st) {
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(few_shared_kernel, dim3((unsigned)(1 + a.S / 8)), dim3(FTHR), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  // two work-groups a CU where their columns fit, and no more than there can be items
-  auto groups = [&](size_t lds, int N) { return std::min(ncu * (lds <= 80 * 1024 ? 2 : 1), a.T * a.k * (N / ROWS)); };
-  const size_t l1 = columns_bytes(a.T, a.L), l2 = columns_bytes(a.T, a.I);
-  if (l1 > 64 * 1024)
-    if ((e = hipFuncSetAttribute(reinterpret_cast<const void *>(&few_expert_kernel<true>),
-                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)l1)) != hipSuccess)
-      return e;
-  if (l2 > 64 * 1024)
-    if ((e = hipFuncSetAttribute(reinterpret_cast<const void *>(&few_expert_kernel<false>),
-                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)l2)) != hipSuccess)
-      return e;
-  const int g1 = groups(l1, a.I), g2 = groups(l2, a.L);
-  hipLaunchKernelGGL(few_expert_kernel<true>, dim3((unsigned)g1), dim3(FTHR), l1, st, a, g1);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(few_expert_kernel<false>, dim3((unsigned)(g2 + a.H / 16 * (a.S > 0))), dim3(FTHR), l2, st, a, g2);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if ((e = launch_expert<true>(a, ncu, a.I, a.L, 0, st)) != hipSuccess) return e;
+  if ((e = launch_expert<false>(a, ncu, a.L, a.I, a.S > 0 ? a.H / 16 : 0, st)) != hipSuccess) return e;
   const int nb = (a.L + CMB - 1) / CMB;
   hipLaunchKernelGGL(few_combine_kernel, dim3((unsigned)nb, (unsigned)a.T), dim3(64), 0, st, a);
   if ((e = hipGetLastError()) != hipSuccess) return e;

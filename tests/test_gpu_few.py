@@ -88,7 +88,9 @@ SHAPES = [LayerShape(256, 128, 32, 4, 128, 1, 128),      # every expert product 
           LayerShape(128, 128, 5, 5, 128, 0, 0),         # every expert, no shared ones
           LayerShape(1024, 640, 33, 1, 256, 1, 1152),    # one expert a token, latent no multiple of 256
           LayerShape(2048, 2048, 64, 4, 1536, 2, 384),
-          LayerShape(512, 1152, 200, 32, 640, 1, 256)]   # the most pairs
+          LayerShape(512, 1152, 200, 32, 640, 1, 256),   # the most pairs
+          LayerShape(256, 3200, 40, 2, 256, 0, 0),       # few long rows: K over a work-group's waves, gate/up
+          LayerShape(128, 256, 24, 1, 2688, 1, 128)]     # and down
 
 
 @pytest.mark.parametrize("T", [1, 2, 3, 4])

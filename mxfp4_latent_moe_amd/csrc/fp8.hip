@@ -580,7 +580,15 @@ hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, h
       else hipLaunchKernelGGL(fp8_join_kernel<float>, jr, dim3(256), 0, st, g, p.splits, partial);
     }
   } else if (g.T <= 16) {
-    stream_by_type<1, 1, 8, 4>(g, e8, out_bf16, st);
+    // Where there are rows enough for a work-group a CU, two row tiles a
+    // work-group halve the tokens' loads, which are as many as the weights';
+    // long rows keep 16 waves busy.  Measured at (tokens, N, K), the three below
+    // in order: (16, 7168, 33792) 61 / 72 / 74 us, (4, 7168, 33792) 53 / 56 / 59,
+    // (16, 6144, 7168) 16.3 / 18.2 / 19.3, (16, 3584, 7168) 14.2 / 10.4 / 11.4,
+    // (1, 7168, 33792) 48.2 / 46.1 / 49.7, (4, 6144, 1024) - / 10.9 / 9.0.
+    if (g.T > 1 && g.N >= 6144) stream_by_type<1, 2, 8, 2>(g, e8, out_bf16, st);
+    else if (g.K >= 4096) stream_by_type<1, 1, 16, 1>(g, e8, out_bf16, st);
+    else stream_by_type<1, 1, 8, 4>(g, e8, out_bf16, st);
   } else if (g.T <= 32) {
     stream_by_type<2, 1, 8, 2>(g, e8, out_bf16, st);
   } else {

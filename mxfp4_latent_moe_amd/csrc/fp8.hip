@@ -591,6 +591,12 @@ hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, h
     else stream_by_type<1, 1, 8, 4>(g, e8, out_bf16, st);
   } else if (g.T <= 32) {
     stream_by_type<2, 1, 8, 2>(g, e8, out_bf16, st);
+  } else if (g.K >= 4096 && (g.N + 15LL) / 16 * ((g.T + 63) / 64) <= 256) {
+    // one row tile a work-group while that is one work-group a CU at most: 33
+    // tokens, 3584 x 7168 16.2 us (with two 19.6), 64 and 895 x 7168 20.6 (23.5);
+    // with 384 work-groups 42 (28.7 at 64 tokens, 6144 x 7168), and short rows
+    // gain nothing (40 tokens, 2048 x 2048 10.6 against 10.0)
+    stream_by_type<4, 1, 8, 1>(g, e8, out_bf16, st);
   } else {
     stream_by_type<4, 2, 8, 1>(g, e8, out_bf16, st);
   }

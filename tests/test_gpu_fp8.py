@@ -92,7 +92,8 @@ def run(mx, T, N, K, kind, out_kind, seed=0, pad=0, opad=0, accumulate=False):
                                    (17, 257, 256), (31, 64, 4112), (33, 100, 384), (64, 255, 640), (65, 384, 400),
                                    (127, 129, 272), (129, 513, 1152), (255, 895, 1024), (257, 256, 128),
                                    (300, 640, 3600), (700, 1100, 528), (70, 130, 16400),
-                                   (7, 6150, 400), (16, 6145, 4128), (9, 50, 4112), (1, 300, 5008)])
+                                   (7, 6150, 400), (16, 6145, 4128), (9, 50, 4112), (1, 300, 5008), (50, 900, 4112),
+                                   (41, 4200, 4112)])
 def test_product(mx, T, N, K, kind):
     out = "bf16" if (T + N) % 2 else "f32"
     say(f"case: 8-bit product T={T} N={N} K={K} scales {kind} out {out}")

@@ -165,13 +165,17 @@ def _norm_out(T, H, device, gamma, n, q, q_scale):
     return o
 
 
+def _raw_stream(device):
+    """The handle of torch.cuda.current_stream(device), without the 1.8 us of making that object."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _enqueue(name, device, stream, *args):
     """One call of the library on `device`: its current stream, or the given one, which must be its own."""
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors must be on a GPU, not {device}")
     if stream is None:
-        # the handle of torch.cuda.current_stream(device), without the 1.8 us of making that object
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        handle = _raw_stream(device)
     elif stream.device != device:
         raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on {device}")
     else:
@@ -515,14 +519,27 @@ class LatentMoE:
         dev = self.w["w_router"].device
         if x.dtype != torch.bfloat16 or not x.is_contiguous() or x.device != dev:
             raise ValueError(f"forward_few: x must be contiguous bfloat16 on {dev}")
-        b = self._few_bufs.get(T)
+        if dev.type != "cuda" or (stream is not None and stream.device != dev):
+            raise ValueError(f"forward_few: tensors on {dev} and stream {stream}, want one GPU")
+        handle = _raw_stream(dev) if stream is None else stream.cuda_stream
+        b, streams = self._few_bufs.get(T) or (None, None)
         if b is None:
             s = self.shape
-            b = self._few_bufs[T] = {
-                "topk_ids": torch.empty((T, s.top_k), dtype=torch.int32, device=dev),
-                "topk_w": torch.empty((T, s.top_k), dtype=torch.float32, device=dev),
-                "out": torch.empty((T, s.hidden), dtype=torch.float32, device=dev),
-                "ws": torch.empty((max(16, layer_few_workspace_bytes(s, T)),), dtype=torch.uint8, device=dev),
-            }
+            # Memory in the order of the stream that will use it: a block of another stream's may still be in use
+            # there.  torch.cuda.stream(None) leaves the current stream.
+            with torch.cuda.stream(stream):
+                b = {
+                    "topk_ids": torch.empty((T, s.top_k), dtype=torch.int32, device=dev),
+                    "topk_w": torch.empty((T, s.top_k), dtype=torch.float32, device=dev),
+                    "out": torch.empty((T, s.hidden), dtype=torch.float32, device=dev),
+                    "ws": torch.empty((max(16, layer_few_workspace_bytes(s, T)),), dtype=torch.uint8, device=dev),
+                }
+            streams = {handle}
+            self._few_bufs[T] = b, streams
+        elif handle not in streams:
+            # a later call's stream: once freed, the buffers are not handed out before it has passed its calls
+            for t in b.values():
+                t.record_stream(torch.cuda.current_stream(dev) if stream is None else stream)
+            streams.add(handle)
         layer_few(self.shape, x, layer_weights(self.w), b["topk_ids"], b["topk_w"], b["out"], b["ws"], stream)
         return b

@@ -279,6 +279,60 @@ def test_python_refusals(mx):
             moe.forward_few(bad)
 
 
+def spans(tensors):
+    return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors]
+
+
+def apart(a, b):
+    return all(hi <= lo2 or hi2 <= lo for lo, hi in a for lo2, hi2 in b)
+
+
+def test_buffers_follow_the_streams_of_the_calls(mx):
+    """The first call for a token count on a side stream takes no memory whose last use may be pending on the current
+    stream; buffers of a dropped layer object are not handed out while a stream that a call ran on still uses them."""
+    sh = SHAPES[1]
+    say("case: few tokens, buffers and streams")
+    made = make(sh, seed=21)
+    w = upload(*made)
+    x = to_dev_bf16(tokens(sh, 2, 5), DEV)
+    want = mx.LatentMoE(mx.shape_of(sh), w, DEV).forward_few(x)["out"].clone()
+    ws = mx.ops.layer_few_workspace_bytes(mx.shape_of(sh), 2)
+    sizes = [2 * sh.top_k * 4] * 2 + [2 * sh.hidden * 4, ws]
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+    def blocks():
+        return [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+
+    free = blocks()
+    at = spans(free)
+    del free  # the current stream's to use again
+    moe = mx.LatentMoE(mx.shape_of(sh), w, DEV)
+    b = moe.forward_few(x, stream=one)
+    assert apart(spans(b.values()), at)
+    one.synchronize()
+    assert torch.equal(b["out"], want)
+    # a call on a second stream, behind other work there; the layer object goes while that is pending
+    with torch.cuda.stream(two):
+        torch.cuda._sleep(200_000_000)
+    moe.forward_few(x, stream=two)
+    at = spans(b.values())
+    del moe, b
+    with torch.cuda.stream(one):
+        new = blocks()
+    pending = not two.query()
+    assert pending and apart(spans(new), at)
+    torch.cuda.synchronize()
+    # without a stream: the one that is current, as it changes
+    moe = mx.LatentMoE(mx.shape_of(sh), w, DEV)
+    for s in (one, two, one):
+        with torch.cuda.stream(s):
+            b = moe.forward_few(x)
+        s.synchronize()
+        assert torch.equal(b["out"], want)
+
+
 @pytest.mark.slow
 @pytest.mark.parametrize("T", [1, 4])
 def test_full_shape(mx, T):

@@ -472,7 +472,7 @@ int moe_fp8_quantize(int T, int K, const void *x, int x_dtype, int64_t ldx, uint
  * operands, a hundredth of the rounding to bf16); out is rounded once.
  * x_scale bytes are 1..247 (moe_fp8_quantize's).  Deterministic.
  * T may be 0; N is free; K is a multiple of 16 (else MOE_ENOTSUP; K up to 2^20,
- * T, N and ldx up to 2^22).
+ * T, N, ldx and ldxs up to 2^22).
  * Workspace: moe_fp8_gemm_workspace_bytes(T, N, K) bytes (0: unsupported sizes).
  * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */
 size_t moe_fp8_gemm_workspace_bytes(int T, int N, int K);

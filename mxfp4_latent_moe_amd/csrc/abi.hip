@@ -507,7 +507,7 @@ static int fp8_gemm_impl(int T, int N, int K, const uint8_t *x, int64_t ldx, con
   if (!aligned16(x) || ldx % 16 || !aligned16(w) || !aligned16(ws) || !aligned(out, dtype_bytes(out_dtype)) ||
       (w_scale_type == MOE_SCALE_F32 && !aligned(w_scale, 4)))
     return MOE_EINVAL;
-  if (ldx > (1 << 22)) return MOE_ENOTSUP;
+  if (ldx > (1 << 22) || ldxs > (1 << 22)) return MOE_ENOTSUP;  // 32-bit offsets within a work-group's rows
   if (ws_bytes < moe_fp8_gemm_workspace_bytes(T, N, K)) return MOE_EWORKSPACE;
   if ((rc = check_device())) return rc;
   if (T == 0) return MOE_OK;

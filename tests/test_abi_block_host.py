@@ -97,6 +97,21 @@ def test_fp8_gemm(lib):
     assert lib.moe_fp8_gemm_workspace_bytes(0, 1, 16) > 0
 
 
+@pytest.mark.parametrize("T", [1, 2, 64, 300])
+def test_fp8_gemm_scale_rows_far_apart(lib, T):
+    """A stride of x_scale with which offsets within a work-group's rows pass 32 bits is refused, as one of x is; the
+    largest that is taken is looked at no further here (the workspace is too small)."""
+    ws = lib.moe_fp8_gemm_workspace_bytes(T, 300, 400)
+
+    def call(ldxs, wsb):
+        return lib.moe_fp8_gemm(T, 300, 400, FAKE, 400, FAKE, ldxs, FAKE, FAKE, _lib.MOE_SCALE_F32, FAKE, F32, 300, 0,
+                                FAKE, wsb, None)
+
+    assert call(1 << 22, ws - 1) == EWS
+    for ldxs in ((1 << 22) + 1, (1 << 32) // 63 + 1, 1 << 32, 1 << 40):
+        assert call(ldxs, ws) == ENOTSUP, ldxs
+
+
 def _shape(**kw):
     sh = synth.K3_SHAPE
     s = _lib.make_shape(sh.hidden, sh.latent, sh.n_experts, sh.top_k, sh.inter, sh.n_shared, sh.shared_inter)

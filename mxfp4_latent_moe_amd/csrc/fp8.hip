@@ -13,6 +13,7 @@
 // instruction, whose sums are fp32 (1e-8 and 8e-8 on the same operands).
 #include <algorithm>
 
+#include "fp8_plan.h"
 #include "kernels.h"
 #include "quant8.h"
 
@@ -506,61 +507,12 @@ void stream_by_type(const Fp8Args &g, bool e8, bool out_bf16, hipStream_t st) {
 
 }  // namespace
 
-// How the tile kernels cut a product, and what it then takes, in us: 8 for the
-// ends of a kernel; of a turn (256 tiles, one a CU) 1.75 a block for tiles of
-// 256 x 256, 1.15 for 256 rows x 128 tokens, 1.45 for 128 x 256 with fp32 sums.
-// The first kind reads least per product, the second fills turns better:
-// 4096 tokens and 6144 rows are 384 of the first (half of the second turn
-// empty, 208 us), 768 of the second (three turns, 210), or 256 of the first and
-// then 256 of the second (193).  Where the tiles are fewer than the CUs, K is
-// split into about one work-group a CU, of four blocks at least, and the parts'
-// sums are written and read at 3 TB/s.
-struct TilePlan {
-  int rows;  // bf16 out: rows in tiles of the first kind
-  int splits;
-  double us;
-};
-static TilePlan tile_plan(int T, int N, int K, bool out_bf16) {
-  const long long kb = (K + 127) / 128, CUS = 256;
-  auto up = [](long long a, long long b) { return (a + b - 1) / b; };
-  const long long small = out_bf16 ? up(N, 256) * up(T, 128) : up(N, 128) * up(T, 256);
-  const double step = out_bf16 ? 1.15 : 1.45;
-  const long long s = std::max(1LL, std::min(std::min(CUS / small, kb / 4), 16LL));
-  TilePlan best{0, (int)s, 8 + step * (double)(up(kb, s) * up(small * s, CUS)) + (s > 1 ? 2.6e-6 * s * T * N : 0.0)};
-  if (!out_bf16 || s > 1) return best;
-  // whole turns of the first kind, or all of it
-  const long long tn = up(N, 256), tt = up(T, 256);
-  for (long long turns = 1; turns <= up(tn * tt, CUS); ++turns) {
-    const long long n = std::min(tn, turns * CUS / tt);
-    if (n == 0) continue;
-    const double us = 8 + (double)kb * (1.75 * (double)up(n * tt, CUS) + step * (double)up((tn - n) * up(T, 128), CUS));
-    if (us < best.us) best = {(int)(256 * n), 1, us};
-  }
-  return best;
-}
-// Whether the stream kernel is faster: its work-groups of 32 rows and 64 tokens
-// take 0.38 us a block, one a CU at a time.  Measured at K = 7168, bf16 out,
-// stream against tiles: 64 tokens and 6144 rows 24 / 22 us, 512 and 895 24 / 29,
-// 128 and 6144 48 / 28, 1024 and 895 46 / 30, 512 and 6144 135 / 47; at K = 512,
-// 300 tokens and 3584 rows, 11 / 17.  Up to 64 tokens it is always taken.
-static bool stream_fits(const TilePlan &tile, int T, int N, int K) {
-  if (T <= 64) return true;
-  const long long groups = (long long)((N + 31) / 32) * ((T + 63) / 64);
-  return 2.5 + 0.38 * ((K + 127) / 128) * (double)((groups + 255) / 256) <= tile.us;
-}
-
-size_t fp8_workspace_bytes(int T, int N, int K) {
-  size_t need = 0;
-  for (const bool out_bf16 : {false, true}) {
-    const TilePlan p = tile_plan(T, N, K, out_bf16);
-    if (!stream_fits(p, T, N, K) && p.splits > 1) need = std::max(need, (size_t)p.splits * T * ((N + 3) / 4) * 16);
-  }
-  return need;
-}
+size_t fp8_workspace_bytes(int T, int N, int K) { return fp8_partial_bytes(T, N, K); }
 
 hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, hipStream_t st) {
-  const TilePlan p = tile_plan(g.T, g.N, g.K, out_bf16);
-  if (!stream_fits(p, g.T, g.N, g.K)) {
+  const Fp8Plan plan = fp8_plan(g.T, g.N, g.K, out_bf16);
+  const TilePlan &p = plan.tile;
+  if (!plan.stream) {
     float *partial = static_cast<float *>(ws);
     auto up8 = [](int v) { return (unsigned)((v + 7) & ~7); };
     const dim3 blk(512);

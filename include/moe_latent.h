@@ -449,8 +449,8 @@ typedef struct {
 int moe_block_post_norm(const moe_post_norm_args *a, void *stream);
 
 /* Rows of fp32 or bf16 values as 8-bit codes with block scales (above).
- *   x [T, ldx], q [T, ldq], q_scale [T, ldqs]; T may be 0; any K.
- * Errors: MOE_EINVAL. */
+ *   x [T, ldx], q [T, ldq], q_scale [T, ldqs]; T may be 0; any K up to 2^30.
+ * Errors: MOE_EINVAL; MOE_ENOTSUP (K > 2^30). */
 int moe_fp8_quantize(int T, int K, const void *x, int x_dtype, int64_t ldx, uint8_t *q, int64_t ldq,
                      uint8_t *q_scale, int64_t ldqs, void *stream);
 

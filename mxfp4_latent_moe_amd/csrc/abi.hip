@@ -394,7 +394,7 @@ static int check_norm_out(const moe_norm_out *o, int H, bool *vec) {
   if ((o->q == nullptr) != (o->q_scale == nullptr)) return MOE_EINVAL;
   if (!aligned(o->gamma, 2) || !aligned(o->n, 2)) return MOE_EINVAL;
   if (o->n && o->ldn < H) return MOE_EINVAL;
-  if (o->q && (o->ldq < H || o->ldqs < (H + 127) / 128)) return MOE_EINVAL;
+  if (o->q && (o->ldq < H || o->ldqs < (H - 1) / 128 + 1)) return MOE_EINVAL;
   *vec = *vec && aligned(o->gamma, 16) && (!o->n || chunked(o->n, o->ldn, 2)) && (!o->q || chunked(o->q, o->ldq, 1));
   return MOE_OK;
 }
@@ -475,9 +475,9 @@ static int post_norm_impl(const moe_post_norm_args *p, void *stream) {
 static int fp8_quantize_impl(int T, int K, const void *x, int x_dtype, int64_t ldx, uint8_t *q, int64_t ldq,
                              uint8_t *q_scale, int64_t ldqs, void *stream) {
   if (T < 0 || K <= 0 || !x || !q || !q_scale || !is_float_dtype(x_dtype)) return MOE_EINVAL;
-  const int kb = (K + 127) / 128;
+  const int kb = (K - 1) / 128 + 1;
   if (ldx < K || ldq < K || ldqs < kb || !aligned(x, dtype_bytes(x_dtype))) return MOE_EINVAL;
-  if ((long long)T * kb > (1LL << 34)) return MOE_ENOTSUP;  // one grid
+  if (K > QUANT_MAX_K) return MOE_ENOTSUP;
   const int rc = check_device();
   if (rc) return rc;
   if (T == 0) return MOE_OK;

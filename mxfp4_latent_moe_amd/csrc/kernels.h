@@ -180,6 +180,7 @@ hipError_t launch_reap_experts(const float *contrib, const int32_t *offsets, int
 
 // ---- norms around the block, 8-bit activations
 constexpr int NORM_MAX_H = 16384;
+constexpr int QUANT_MAX_K = 1 << 30;  // positions in a row are 32 bits
 // the forms a normed row is written in: bf16 (n) and / or e4m3 codes with a
 // scale byte per 128 channels (q, qs); leading dimensions in elements
 struct NormOut {

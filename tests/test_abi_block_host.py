@@ -73,6 +73,8 @@ def test_fp8_quantize(lib):
     for bad in (dict(T=-1), dict(K=0), dict(x=None), dict(q=None), dict(s=None), dict(dt=3), dict(ldx=199),
                 dict(ldq=199), dict(lds=1), dict(x=FAKE + 2), dict(dt=BF16, x=FAKE + 1)):
         assert call(**bad) == EINVAL, bad
+    for k in ((1 << 30) + 1, 2 ** 31 - 1):
+        assert call(K=k, ldx=k, ldq=k, lds=k) == ENOTSUP, k
 
 
 def test_fp8_gemm(lib):

@@ -285,6 +285,63 @@ def test_rows_past_32_bit_offsets(mx):
     assert (s[-3:].cpu().numpy() == sb).all()
 
 
+def repeated(small, T):
+    """Row t of the result is row t % 7 of small."""
+    return small.repeat(-(-T // 7), *[1] * (small.dim() - 1))[:T]
+
+
+# more rows than one launch of 128 (512) threads a row holds
+@pytest.mark.parametrize("T,H", [(2 ** 25 + 5, 1), (2 ** 23 + 3, 1032)])
+def test_pre_norm_of_many_rows(mx, T, H):
+    """A row's result does not depend on the others: seven rows over and over against the seven alone, bit for bit."""
+    say(f"case: pre norm T={T} H={H}")
+    few = rows(7, H, torch.bfloat16, 0, seed=H)
+    gamma = (1 + 0.1 * torch.randn(H, generator=torch.Generator().manual_seed(1))).to(torch.bfloat16).to(DEV)
+    kb = -(-H // 128)
+    got = []
+    for x in (few.contiguous(), repeated(few, T)):
+        t = x.shape[0]
+        o = (torch.zeros((t, H), dtype=torch.bfloat16, device=DEV), torch.zeros((t, H), dtype=torch.uint8, device=DEV),
+             torch.zeros((t, kb), dtype=torch.uint8, device=DEV))
+        mx.block_pre_norm(x, gamma, 1.0, n=o[0], q=o[1], q_scale=o[2])
+        got.append(o)
+    del x
+    for a, b in zip(*got):
+        assert torch.equal(repeated(a, T), b)
+
+
+def test_post_norm_of_many_rows(mx):
+    T, H = 2 ** 25 + 5, 2
+    say(f"case: post norm T={T} H={H}")
+    few = [rows(7, H, torch.float32, 0, seed=i) for i in (1, 2)] + [rows(7, 1, torch.float32, 0, seed=3)]
+    gamma = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    got = []
+    for y, r, g in (tuple(v.contiguous() for v in few), tuple(repeated(v, T) for v in few)):
+        t = y.shape[0]
+        n = torch.zeros((t, H), dtype=torch.bfloat16, device=DEV)
+        mx.block_post_norm(y, r, r, gamma=gamma, gate=g, scale=0.5, eps=1.0, next_gamma=gamma, n=n)  # in place
+        full = torch.zeros_like(r)
+        mx.block_post_norm(y, r, full, gate=y, gate_sigmoid=True)
+        got.append((r, n, full))
+    for a, b in zip(*got):
+        assert torch.equal(repeated(a, T), b)
+
+
+@pytest.mark.parametrize("T,K", [(2 ** 28 + 17, 1), (2 ** 27 + 9, 130)])
+def test_quantize_of_many_blocks(mx, T, K):
+    say(f"case: quantize T={T} K={K}")
+    few = rows(7, K, torch.bfloat16, 0, seed=K)
+    kb = -(-K // 128)
+    got = []
+    for x in (few.contiguous(), repeated(few, T)):
+        o = [torch.zeros((x.shape[0], n), dtype=torch.uint8, device=DEV) for n in (K, kb)]
+        mx.fp8_quantize(x, *o)
+        got.append(o)
+    del x
+    for a, b in zip(*got):
+        assert torch.equal(repeated(a, T), b)
+
+
 def test_python_refusals(mx):
     gamma = torch.ones(64, dtype=torch.bfloat16, device=DEV)
     x = torch.zeros((2, 64), device=DEV)

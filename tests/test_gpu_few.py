@@ -123,6 +123,30 @@ def test_longest_rows(mx, sh):
         check(moe.forward_few(to_dev_bf16(x, DEV)), oracle(x, dense, bias, stack, sh), x, moe)
 
 
+# K over a work-group's waves, where the sums and the columns take more than 64 KB of LDS together, and more than 60
+# for the columns alone; gate/up and down
+SPLIT_LONG = [LayerShape(128, 4224, 10, 2, 256, 0, 0), LayerShape(128, 8192, 6, 2, 256, 1, 128),
+              LayerShape(128, 256, 10, 1, 4224, 1, 128), LayerShape(128, 256, 6, 2, 8192, 0, 0)]
+
+
+@pytest.mark.parametrize("sh", SPLIT_LONG + SHAPES[-2:], ids=lambda s: f"L{s.latent}I{s.inter}")
+def test_split_rows(mx, sh):
+    """Long rows split over the waves against the oracle; a token's result is the same alone and in company."""
+    say(f"case: few tokens, rows split over the waves, {sh}")
+    dense, bias, stack = make(sh, seed=17)
+    moe = mx.LatentMoE(mx.shape_of(sh), upload(dense, bias, stack), DEV)
+    x = tokens(sh, 4, 18)
+    ref = oracle(x, dense, bias, stack, sh)
+    alone = []
+    for t in range(4):
+        alone.append(moe.forward_few(to_dev_bf16(x[t:t + 1], DEV))["out"][0].clone())
+    for T in (1, 2, 3, 4):
+        b = moe.forward_few(to_dev_bf16(x[:T], DEV))
+        check(b, {k: ref[k][:T] for k in ("ids", "weights", "out", "gap")}, x[:T], moe)
+        for t in range(T):
+            assert torch.equal(b["out"][t], alone[t])
+
+
 def test_matches_the_chain_of_calls(mx):
     sh = SHAPES[4]
     dense, bias, stack = make(sh, seed=11)

@@ -63,3 +63,9 @@ def test_every_plan_covers_its_product(plan):
 
 def test_no_tokens_need_no_plan(plan):
     assert plan([(0, 3584, 7168)]) == [(0, 1, 0, 1, 1, 0, 1)]
+
+
+def test_sizes_of_the_parts_tests(plan):
+    """The sizes with which the GPU tests mean to split K, in both outputs."""
+    for need, s32, _, k32, s16, _, k16 in plan([(301, 895, 7168), (301, 893, 7168), (130, 3002, 4112)]):
+        assert not s32 and not s16 and k32 > 1 and k16 > 1 and need > 0

@@ -3,7 +3,9 @@
     python -m mxfp4_latent_moe_amd.build
 
 Every source is compiled for gfx950 only, with packed fp32 ops disabled
-(`-Xclang -target-feature -Xclang -packed-fp32-ops`).
+(`-Xclang -target-feature -Xclang -packed-fp32-ops`).  The assembly of the
+kernels that pace their LDS reads by hand is checked (asm_check.py): a build in
+which a register is used before its read has landed fails.
 """
 from __future__ import annotations
 
@@ -12,6 +14,8 @@ import shutil
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
+
+from .asm_check import unsafe_reads
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +28,7 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["abi.hip", "gemm.hip", "stream.hip", "grouped_stream.hip", "prefill.hip", "route.hip",
            "permute.hip", "combine.hip", "mx8.hip", "dense.hip", "reap.hip", "prefill_pl.hip",
            "block.hip", "fp8.hip", "few.hip"]
+CHECKED = ["dense.hip", "fp8.hip", "prefill.hip", "prefill_pl.hip"]  # issue LDS reads in inline assembly
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -49,6 +54,15 @@ def _run(cmd, verbose):
         print(out)
 
 
+def _check(src):
+    path = os.path.join(BUILD, os.path.splitext(src)[0] + "-hip-amdgcn-amd-amdhsa-gfx950.s")
+    with open(path) as f:
+        bad = unsafe_reads(f.read())
+    if bad:
+        raise RuntimeError(f"{src}: registers used before their LDS read has landed:\n"
+                           + "\n".join(f"  {name}, line {no}: {text}" for name, no, text in bad[:20]))
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -58,9 +72,12 @@ def build(verbose: bool = False) -> str:
     for src in SOURCES:
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         objs.append(obj)
-        cmds.append([cc, *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj])
+        keep = ["-save-temps=obj"] if src in CHECKED else []
+        cmds.append([cc, *HIPCC_FLAGS, *keep, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj])
     with ThreadPoolExecutor(min(len(cmds), os.cpu_count() or 1)) as ex:
         list(ex.map(lambda c: _run(c, verbose), cmds))
+    for src in CHECKED:
+        _check(src)
     tmp = LIB + ".tmp"
     _run([cc, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp], verbose)
     os.replace(tmp, LIB)

@@ -365,6 +365,7 @@ class LatentMoE:
         self.device = torch.device(device)
         self._bufs: dict = {}
         self._few_bufs: dict = {}
+        self._streams: dict = {}  # handles of the streams that buffers were made for or used on
         self.overlap_shared = overlap_shared
         # at decode sizes the latent projection z joins the shared experts on
         # the side stream, so the main stream's routing is only the router and
@@ -416,6 +417,7 @@ class LatentMoE:
             "ws_shared": torch.empty((ws_sh,), dtype=torch.uint8, device=dev),
         }
         self._bufs[T] = b
+        self._streams["forward", T] = {torch.cuda.current_stream(dev).cuda_stream}
         return b
 
     def forward(self, x: torch.Tensor, stream=None, marks: list | None = None, mark_names=None) -> dict:
@@ -425,9 +427,11 @@ class LatentMoE:
         s, w = self.shape, self.w
         T = x.shape[0]
         P = T * s.top_k
-        b = self.buffers(T)
+        with torch.cuda.stream(stream):  # new memory in the order of the call's stream; None: the current one
+            b = self.buffers(T)
         ws = b["ws"]
         st = torch.cuda.current_stream() if stream is None else stream
+        self._uses("forward", T, b, st.cuda_stream, st)
         side = self.side if self.overlap_shared else st
 
         def call(name, strm, fn):
@@ -505,6 +509,27 @@ class LatentMoE:
                                      1 if shared else 0, ws, st))
         return b
 
+    def _few_buffers(self, T: int, dev) -> dict:
+        s = self.shape
+        b = self._few_bufs[T] = {
+            "topk_ids": torch.empty((T, s.top_k), dtype=torch.int32, device=dev),
+            "topk_w": torch.empty((T, s.top_k), dtype=torch.float32, device=dev),
+            "out": torch.empty((T, s.hidden), dtype=torch.float32, device=dev),
+            "ws": torch.empty((max(16, layer_few_workspace_bytes(s, T)),), dtype=torch.uint8, device=dev),
+        }
+        self._streams["few", T] = {_raw_stream(dev)}
+        return b
+
+    def _uses(self, form: str, T: int, bufs: dict, handle: int, stream):
+        """A call on a stream (None: the current one) uses the buffers: once freed, their memory is not handed out
+        before every stream that calls ran on has passed them."""
+        streams = self._streams[form, T]
+        if handle in streams:
+            return
+        for t in bufs.values():
+            t.record_stream(torch.cuda.current_stream(t.device) if stream is None else stream)
+        streams.add(handle)
+
     def forward_few(self, x: torch.Tensor, stream=None) -> dict:
         """The layer for up to MOE_FEW_MAX_T tokens (x [T, H] bf16) as one call of six kernels on one stream: for
         single tokens and drafts, where the time of forward() goes into the steps between the weight streams.
@@ -521,25 +546,10 @@ class LatentMoE:
             raise ValueError(f"forward_few: x must be contiguous bfloat16 on {dev}")
         if dev.type != "cuda" or (stream is not None and stream.device != dev):
             raise ValueError(f"forward_few: tensors on {dev} and stream {stream}, want one GPU")
-        handle = _raw_stream(dev) if stream is None else stream.cuda_stream
-        b, streams = self._few_bufs.get(T) or (None, None)
+        b = self._few_bufs.get(T)
         if b is None:
-            s = self.shape
-            # Memory in the order of the stream that will use it: a block of another stream's may still be in use
-            # there.  torch.cuda.stream(None) leaves the current stream.
-            with torch.cuda.stream(stream):
-                b = {
-                    "topk_ids": torch.empty((T, s.top_k), dtype=torch.int32, device=dev),
-                    "topk_w": torch.empty((T, s.top_k), dtype=torch.float32, device=dev),
-                    "out": torch.empty((T, s.hidden), dtype=torch.float32, device=dev),
-                    "ws": torch.empty((max(16, layer_few_workspace_bytes(s, T)),), dtype=torch.uint8, device=dev),
-                }
-            streams = {handle}
-            self._few_bufs[T] = b, streams
-        elif handle not in streams:
-            # a later call's stream: once freed, the buffers are not handed out before it has passed its calls
-            for t in b.values():
-                t.record_stream(torch.cuda.current_stream(dev) if stream is None else stream)
-            streams.add(handle)
+            with torch.cuda.stream(stream):  # the memory in the order of the call's stream; None: the current one
+                b = self._few_buffers(T, dev)
+        self._uses("few", T, b, _raw_stream(dev) if stream is None else stream.cuda_stream, stream)
         layer_few(self.shape, x, layer_weights(self.w), b["topk_ids"], b["topk_w"], b["out"], b["ws"], stream)
         return b

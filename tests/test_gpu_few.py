@@ -357,6 +357,44 @@ def test_buffers_follow_the_streams_of_the_calls(mx):
         assert torch.equal(b["out"], want)
 
 
+@pytest.mark.parametrize("T", [2, 96])
+def test_buffers_of_the_chain_of_calls(mx, T):
+    """As test_buffers_follow_the_streams_of_the_calls, for forward()."""
+    sh = SHAPES[1]
+    say(f"case: forward(), buffers and streams, T={T}")
+    w = upload(*make(sh, seed=22))
+    x = to_dev_bf16(tokens(sh, T, 6), DEV)
+    first = mx.LatentMoE(mx.shape_of(sh), w, DEV).forward(x)
+    want = first["out"].clone()
+    sizes = [t.numel() * t.element_size() for t in first.values()]
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del first
+    torch.cuda.empty_cache()
+
+    def blocks():
+        return [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+
+    free = blocks()
+    at = spans(free)
+    del free
+    moe = mx.LatentMoE(mx.shape_of(sh), w, DEV)
+    b = moe.forward(x, stream=one)
+    assert apart(spans(b.values()), at)
+    one.synchronize()
+    assert torch.equal(b["out"], want)
+    with torch.cuda.stream(two):
+        torch.cuda._sleep(200_000_000)
+    moe.forward(x, stream=two)
+    at = spans(b.values())
+    del moe, b
+    with torch.cuda.stream(one):
+        new = blocks()
+    pending = not two.query()
+    assert pending and apart(spans(new), at)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.slow
 @pytest.mark.parametrize("T", [1, 4])
 def test_full_shape(mx, T):

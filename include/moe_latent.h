@@ -466,11 +466,13 @@ int moe_fp8_quantize(int T, int K, const void *x, int x_dtype, int64_t ldx, uint
  *   w_scale [N / 128, K / 128], both rounded up: one scale per 128 x 128 block,
  *           fp32 or e8m0 bytes
  *   out     [T, ldo]  fp32 (written, or added to with accumulate = 1) or bf16
- * fp32 out: products are exact and sums fp32.  bf16 out may use the 8-bit
- * matrix instructions, which drop what lies some 14 bits below a group's
- * largest product (1.5e-5 of the result's rms on normally distributed
+ * fp32 out: products are exact and sums fp32.  bf16 out of more than 64 tokens
+ * may use the 8-bit matrix instructions, which drop what lies some 14 bits below
+ * a group's largest product (1.5e-5 of the result's rms on normally distributed
  * operands, a hundredth of the rounding to bf16); out is rounded once.
- * x_scale bytes are 1..247 (moe_fp8_quantize's).  Deterministic.
+ * x_scale bytes are 1..247 (moe_fp8_quantize's).  A block's two scales may be
+ * multiplied before they meet its sum, in fp32: where that product leaves the
+ * range it is infinite (and NaN against a sum of zero) or zero.  Deterministic.
  * T may be 0; N is free; K is a multiple of 16 (else MOE_ENOTSUP; K up to 2^20,
  * T, N, ldx and ldxs up to 2^22).
  * Workspace: moe_fp8_gemm_workspace_bytes(T, N, K) bytes (0: unsupported sizes).

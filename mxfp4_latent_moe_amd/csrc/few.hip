@@ -23,12 +23,14 @@
 // Every sum has one order, so results do not depend on the schedule.
 //
 // Measured (hidden 7168, latent 3584, 16 of 896 experts of 3072, 6144 shared):
-// 155 us for one token, 218 for two, 305 for four, 4.3 to 4.8 TB/s of the bytes
-// the layer cannot do without; the layer's calls one by one take 181, 224 and
-// 319.  Of the 155 us about 4 a kernel are the launch and its cold code, and
-// gate/up runs at 5.8 TB/s at four tokens.  One resident kernel that hands work
-// items from step to step by counters in place of launches took 177, 247 and
-// 350 us: its waves could not keep the weights flowing through the steps' ends.
+// 157 us for one token, 224 for two, 303 to 315 for four, 4.2 to 4.8 TB/s of the
+// bytes the layer cannot do without; the layer's calls one by one take 181, 230
+// and 318.  Of the 157 us about 4 a kernel are the launch and its cold code, and
+// some more go to work-groups that do not divide over the CUs: of gate/up's 384
+// half of the CUs have two and the others one (48 us, 3.9 TB/s; at four tokens,
+// with some 61 distinct experts, 5.2).  One resident kernel that hands work items
+// from step to step by counters in place of launches took 177, 247 and 350 us:
+// its waves could not keep the weights flowing through the steps' ends.
 // Requests further ahead are no faster: two groups of K steps ahead in the
 // expert products 50 against 46 us at one token (one work-group a CU fits), and
 // in the bf16 products four steps a round 58 against 38.

@@ -195,15 +195,17 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(Fp8Args g) {
 // onto the fp32 sum, between the next tokens' products.  Without F8 the codes go
 // through the bf16 instruction.
 //
-// 4096 x 6144 x 7168: 193 us to bf16 with fp32 scales (1.87 PFLOP/s), 169 with
-// e8m0 scales (2.13), 360 to fp32 (1.0; the library's bf16 product of 8192^3
-// runs at 1.25, its 8-bit one without block scales takes 154 us here).  What
-// bounds the first: the same without the multiply-adds takes 169; without loads
-// and barriers, 165 (products, multiply-adds and LDS reads: the 8-bit
-// instructions alone, fed from LDS one read each, reach 3.0 PFLOP/s, 120 us).
-// Tried and slower: weights straight to the registers of the one wave that needs
-// them (291 us: such a load touches 16 rows for 64 bytes each), 192 rows a tile
-// (205), all of a block's loads at its start (+9).
+// 4096 x 6144 x 7168, the kernel alone, call after call, by card: 173 to 187 us
+// to bf16 with fp32 scales (1.9 to 2.1 PFLOP/s), 162 to 174 with e8m0 scales
+// (2.1 to 2.2), 327 to 343 to fp32 (1.05 to 1.1; the library's bf16 product of
+// 8192^3 runs at 1.25, its 8-bit one without block scales takes 154 us here).
+// What bounds the first is the issue of products and multiply-adds: without the
+// latter (e8m0 scales) it is 11 us shorter, a third of the waves' cycles wait
+// for an issue slot, and the 8-bit instructions are busy for 48 % of them; alone,
+// fed from LDS one read each, these reach 3.0 PFLOP/s, 120 us.  Tried and slower,
+// at a time when the kernel took 193 to 199: weights straight to the registers of
+// the one wave that needs them (291: such a load touches 16 rows for 64 bytes
+// each), 192 rows a tile (205), all of a block's loads at its start (+9).
 constexpr int SCB = 8;   // blocks whose scales are in LDS at a time
 
 // 16 bytes of LDS at a + O, issued without waiting
@@ -532,9 +534,10 @@ hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, h
       else hipLaunchKernelGGL(fp8_join_kernel<float>, jr, dim3(256), 0, st, g, p.splits, partial);
     }
   } else if (g.T <= 16) {
-    // Where there are rows enough for a work-group a CU, two row tiles a
-    // work-group halve the tokens' loads, which are as many as the weights';
-    // long rows keep 16 waves busy.  Measured at (tokens, N, K), the three below
+    // Two row tiles a work-group halve the tokens' loads, which are as many as the
+    // weights', where rows are many: 6144 (192 work-groups) is the fewest at which
+    // that was measured faster, 3584 the most at which it was slower.  Long rows
+    // keep 16 waves busy.  Measured at (tokens, N, K), the three below
     // in order: (16, 7168, 33792) 61 / 72 / 74 us, (4, 7168, 33792) 53 / 56 / 59,
     // (16, 6144, 7168) 16.3 / 18.2 / 19.3, (16, 3584, 7168) 14.2 / 10.4 / 11.4,
     // (1, 7168, 33792) 48.2 / 46.1 / 49.7, (4, 6144, 1024) - / 10.9 / 9.0.
@@ -545,8 +548,8 @@ hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, h
     stream_by_type<2, 1, 8, 2>(g, e8, out_bf16, st);
   } else if (g.K >= 4096 && (g.N + 15LL) / 16 * ((g.T + 63) / 64) <= 256) {
     // one row tile a work-group while that is one work-group a CU at most: 33
-    // tokens, 3584 x 7168 16.2 us (with two 19.6), 64 and 895 x 7168 20.6 (23.5);
-    // with 384 work-groups 42 (28.7 at 64 tokens, 6144 x 7168), and short rows
+    // tokens, 3584 x 7168 16.4 us (with two 19.6), 64 and 895 x 7168 20.2 (23.5);
+    // with 384 work-groups 42 (28.2 at 64 tokens, 6144 x 7168), and short rows
     // gain nothing (40 tokens, 2048 x 2048 10.6 against 10.0)
     stream_by_type<4, 1, 8, 1>(g, e8, out_bf16, st);
   } else {

@@ -11,9 +11,9 @@ namespace moe {
 // ends of a kernel; of a turn (256 tiles, one a CU) 1.75 a block for tiles of
 // 256 x 256, 1.15 for 256 rows x 128 tokens, 1.45 for 128 x 256 with fp32 sums.
 // The first kind reads least per product, the second fills turns better:
-// 4096 tokens and 6144 rows are 384 of the first (half of the second turn
-// empty, 208 us), 768 of the second (three turns, 210), or 256 of the first and
-// then 256 of the second (193).  Where the tiles are fewer than the CUs, K is
+// 4096 tokens and 6144 rows of 7168 are 384 of the first (half of the second
+// turn empty, 207 us), 768 of the second (three turns, 199), or 256 of the first
+// and then 256 of the second (186, all on one card).  Where the tiles are fewer than the CUs, K is
 // split into about one work-group a CU, of four blocks at least, and the parts'
 // sums are written and read at 3 TB/s.
 struct TilePlan {
@@ -39,11 +39,14 @@ inline TilePlan tile_plan(int T, int N, int K, bool out_bf16) {
   }
   return best;
 }
-// Whether the stream kernel is faster: its work-groups of 32 rows and 64 tokens
-// take 0.38 us a block, one a CU at a time.  Measured at K = 7168, bf16 out,
-// stream against tiles: 64 tokens and 6144 rows 24 / 22 us, 512 and 895 24 / 29,
-// 128 and 6144 48 / 28, 1024 and 895 46 / 30, 512 and 6144 135 / 47; at K = 512,
-// 300 tokens and 3584 rows, 11 / 17.  Up to 64 tokens it is always taken.
+// Whether the stream kernel is taken above 64 tokens: its work-groups of 32 rows
+// and 64 tokens take 0.38 us a block, one a CU at a time.  Measured at K = 7168,
+// stream against tiles in us, (tokens, rows), bf16 out then fp32 out:
+// (128, 6144) 48 / 27, 48 / 34; (512, 6144) 137 / 43, 136 / 66; (1024, 895)
+// 46 / 25, 46 / 30; (301, 895) 23.8 / 21.7, 23.9 / 25.1; (512, 895) 24.5 / 23,
+// 25 / 27; at K = 512 (300, 3584) 11 / 11, 11 / 14.  Where they are within some
+// 5 % of each other the rule may take the slower: it does at (301, 895) to fp32
+// and at (512, 895) to bf16.
 inline bool stream_fits(const TilePlan &tile, int T, int N, int K) {
   const long long groups = (long long)((N + 31) / 32) * ((T + 63) / 64);
   return 2.5 + 0.38 * ((K + 127) / 128) * (double)((groups + 255) / 256) <= tile.us;
@@ -54,6 +57,11 @@ struct Fp8Plan {
   TilePlan tile;  // unless stream
 };
 inline Fp8Plan fp8_plan(int T, int N, int K, bool out_bf16) {
+  // Up to 64 tokens the stream kernel, whose sums are fp32 in both outputs, so
+  // that decode batches of any size round alike.  To fp32 the tiles are no
+  // faster where there are rows ((64, 6144) 28 / 30 us, (33, 3584) 16.4 / 20.7);
+  // to bf16 they are from about 64 tokens on ((64, 6144) 28 / 21, (64, 895)
+  // 20 / 15, (33, 3584) 16.5 / 15.5).
   if (T <= 64) return {true, {}};
   const TilePlan tile = tile_plan(T, N, K, out_bf16);
   return {stream_fits(tile, T, N, K), tile};

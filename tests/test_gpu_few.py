@@ -147,6 +147,58 @@ def test_split_rows(mx, sh):
             assert torch.equal(b["out"][t], alone[t])
 
 
+@pytest.mark.parametrize("sh", [LayerShape(65536, 128, 6, 2, 128, 1, 128), LayerShape(128, 128, 6, 2, 128, 1, 65536),
+                                LayerShape(128, 128, 1024, 32, 128, 0, 0)], ids=["hidden", "shared", "experts"])
+def test_largest_sizes(mx, sh):
+    """The widest hidden and shared layers (one or two sums of 65536 terms, 46 2^-24 each by the rule above, beside
+    short ones of under 4: no more than five of 24), and the most experts and choices."""
+    say(f"case: few tokens {sh}")
+    dense, bias, stack = make(sh, seed=19)
+    moe = mx.LatentMoE(mx.shape_of(sh), upload(dense, bias, stack), DEV)
+    for T in (1, 4):
+        x = tokens(sh, T, seed=60 + T)
+        check(moe.forward_few(to_dev_bf16(x, DEV)), oracle(x, dense, bias, stack, sh), x, moe)
+
+
+def test_without_the_routing(mx):
+    """The call that does not ask for ids and weights."""
+    sh = SHAPES[1]
+    say("case: few tokens, ids and weights not asked for")
+    w = upload(*make(sh, seed=23))
+    shape = mx.shape_of(sh)
+    x = to_dev_bf16(tokens(sh, 3, 2), DEV)
+    want = mx.LatentMoE(shape, w, DEV).forward_few(x)["out"]
+    out = torch.empty_like(want)
+    ws = torch.full((mx.ops.layer_few_workspace_bytes(shape, 3),), 0xFF, dtype=torch.uint8, device=DEV)
+    mx.ops.layer_few(shape, x, mx.ops.layer_weights(w), None, None, out, ws)
+    assert torch.equal(out, want)
+
+
+def test_first_call_in_a_capture(mx):
+    """Buffers made while a graph is captured serve its replays and eager calls after it."""
+    sh = SHAPES[1]
+    say("case: few tokens, the first call captured")
+    w = upload(*make(sh, seed=24))
+    moe, eager = (mx.LatentMoE(mx.shape_of(sh), w, DEV) for _ in range(2))
+    x = to_dev_bf16(tokens(sh, 2, 7), DEV)
+    eager.forward_few(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b = moe.forward_few(x)
+    for k in range(3):
+        x.copy_(to_dev_bf16(tokens(sh, 2, 200 + k), DEV))
+        want = eager.forward_few(x)["out"].clone()
+        b["out"].fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(b["out"], want)
+        b["out"].fill_(float("nan"))
+        assert moe.forward_few(x)["out"] is b["out"]
+        torch.cuda.synchronize()
+        assert torch.equal(b["out"], want)
+
+
 def test_matches_the_chain_of_calls(mx):
     sh = SHAPES[4]
     dense, bias, stack = make(sh, seed=11)

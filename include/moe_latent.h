@@ -73,6 +73,7 @@ extern "C" {
 #define MOE_DT_F32 0
 #define MOE_DT_BF16 1
 #define MOE_DT_BF16X2 2 /* bf16 planes: row r holds hi[0..K) then lo[0..K) */
+#define MOE_DT_MXFP4 3  /* e2m1 codes and scale bytes (an output of moe_mxfp4_expert_gemm) */
 
 /* moe_workspace_bytes() function selectors */
 #define MOE_FN_ROUTE 0
@@ -481,6 +482,91 @@ size_t moe_fp8_gemm_workspace_bytes(int T, int N, int K);
 int moe_fp8_gemm(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8_t *x_scale, int64_t ldxs,
                  const uint8_t *w, const void *w_scale, int w_scale_type, void *out, int out_dtype, int64_t ldo,
                  int accumulate, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- MXFP4 rows, and products with both operands in MXFP4.
+ *
+ * MXFP4: e2m1 codes packed two to a byte, element 2b in the low nibble of byte
+ * b, and one scale byte per row and block of 32 consecutive values (the last
+ * block may be shorter): a value is code * 2^(byte - 127), as in the expert
+ * weights.  Two rules for the scale 2^e of a block whose largest magnitude is
+ * amax: */
+#define MOE_MX_SCALE_FIT 0 /* the smallest 2^e with amax <= 6 2^e: nothing saturates */
+#define MOE_MX_SCALE_OCP 1 /* 2^(floor(log2 amax) - 2), OCP MX v1.0: magnitudes above 6 2^e become 6 2^e */
+/* Scale bytes written are 2..253 (2 for a block of zeros); values are rounded
+ * to nearest, ties to even.  A block that holds a value that is not finite gets
+ * the scale byte 255 (NaN) and codes of zero. */
+
+/* Rows of fp32 or bf16 values in MXFP4.
+ *   x [T, ldx]; q [T, ldq] bytes, ldq >= K / 2 rounded up; q_scale [T, ldqs]
+ * T may be 0; any K up to 2^30 (the high nibble past an odd K is zero).  Rows
+ * whose width is a multiple of 8, 16-byte aligned in x and 4-byte aligned in q,
+ * are moved in vectors, others value by value.
+ * Errors: MOE_EINVAL; MOE_ENOTSUP (K > 2^30). */
+int moe_mxfp4_quantize(int T, int K, const void *x, int x_dtype, int64_t ldx, int scale_rule, uint8_t *q, int64_t ldq,
+                       uint8_t *q_scale, int64_t ldqs, void *stream);
+
+/* MXFP4 rows as fp32 or bf16 values, exact where the type holds them (bf16: any
+ * scale byte; above 252 large codes are infinite).  A scale byte of 255 gives
+ * NaN.  Sizes, strides and errors as for moe_mxfp4_quantize. */
+int moe_mxfp4_dequantize(int T, int K, const uint8_t *q, int64_t ldq, const uint8_t *q_scale, int64_t ldqs, void *out,
+                         int out_dtype, int64_t ldo, void *stream);
+
+/* Dense product of MXFP4 activations and MXFP4 weights:
+ *   out[t, n] (+)= sum_k x[t, k] w[n, k]
+ *   x       [T, ldx]  codes, ldx bytes a row, a multiple of 16
+ *   x_scale [T, ldxs] scale bytes
+ *   w       [N, K/2], w_scale [N, K/32]
+ *   out     [T, ldo]  fp32 (written, or added to with accumulate = 1) or bf16
+ * Products are exact and sums fp32 in both outputs; bf16 is rounded once.  Scale
+ * bytes are 0..254; 255 gives NaN in its row or column.  Where the product of a
+ * block's two scales leaves fp32's range the result is unspecified.
+ * Deterministic.  T may be 0; N is free; K is a multiple of 32 (else
+ * MOE_ENOTSUP; T up to 2^21, N and K up to 2^20, ldx and ldxs up to 2^22).
+ * Workspace: moe_mxfp4_gemm_workspace_bytes(T, N, K) bytes (0: unsupported).
+ * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */
+size_t moe_mxfp4_gemm_workspace_bytes(int T, int N, int K);
+int moe_mxfp4_gemm(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8_t *x_scale, int64_t ldxs,
+                   const uint8_t *w, const uint8_t *w_scale, void *out, int out_dtype, int64_t ldo, int accumulate,
+                   void *ws, size_t ws_bytes, void *stream);
+
+typedef struct {
+  int32_t n_experts, P, N, K;    /* P: rows of out (sorted rows) */
+  const int32_t *expert_offsets; /* [E+1]: expert e owns sorted rows offsets[e] .. offsets[e+1] */
+  const uint8_t *x;              /* codes [x_rows, ldx] */
+  int64_t ldx;
+  const uint8_t *x_scale;        /* [x_rows, ldxs] */
+  int64_t ldxs;
+  int32_t x_rows;
+  int32_t top_k;                 /* > 0: sorted row p reads x row sorted_pair[p] / top_k; 0: row p */
+  const int32_t *sorted_pair;    /* [P], needed with top_k > 0 or pair_weight */
+  const uint8_t *w, *w_scale;    /* [E, N, K/2], [E, N, K/32] */
+  const uint8_t *w3, *w3_scale;  /* both or neither: out = SiTU-GLU(x w^T, x w3^T) */
+  float beta, beta_lin;          /* of SiTU-GLU */
+  const float *pair_weight;      /* sorted row p is scaled by pair_weight[sorted_pair[p]]; NULL: not; not with w3 */
+  void *out;
+  int64_t ldo;                   /* elements, >= N; MOE_DT_MXFP4: bytes, >= N/2 and a multiple of 16 */
+  int32_t out_dtype;             /* MOE_DT_F32, MOE_DT_BF16, or with w3 MOE_DT_MXFP4 */
+  uint8_t *out_scale;            /* [P, ldos], exactly with MOE_DT_MXFP4 */
+  int64_t ldos;
+} moe_mxfp4_expert_args;
+
+/* The routed experts' products on MXFP4 rows, with mxfp4_grouped_gemm's
+ * weights, sorted rows and SiTU-GLU.  Where that call takes the activations at
+ * bf16 hi + lo or fp32 precision, here they are MXFP4 rows (moe_mxfp4_quantize:
+ * each token's row once, gathered here), and the gate and up call can write its
+ * result in MXFP4 (MOE_MX_SCALE_FIT, from the fp32 value) for the down call.
+ * Products are exact, sums and SiTU-GLU fp32, other outputs rounded once.
+ * Rows of out from expert_offsets[E] on are left as they were; experts without
+ * rows cost nothing; nothing waits on the host.  Device preconditions:
+ * ascending offsets from 0 to at most P, sorted_pair[p] / top_k in [0, x_rows).
+ * Deterministic.  Limits (else MOE_ENOTSUP): K a multiple of 32, N too with
+ * MOE_DT_MXFP4; at most 1024 experts; P up to 2^21, N and K up to 2^20, ldx and
+ * ldxs up to 2^22; gathered, x_rows * ldx and x_rows * ldxs below 2^31.  P may
+ * be 0.  Workspace: moe_mxfp4_expert_gemm_workspace_bytes(E, P, N, K) bytes (0:
+ * unsupported).
+ * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */
+size_t moe_mxfp4_expert_gemm_workspace_bytes(int E, int P, int N, int K);
+int moe_mxfp4_expert_gemm(const moe_mxfp4_expert_args *a, void *ws, size_t ws_bytes, void *stream);
 
 /* every weight of a layer, as the calls above take them */
 typedef struct {

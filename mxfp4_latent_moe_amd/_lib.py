@@ -15,20 +15,23 @@ LIB_PATH = os.path.join(PKG, "lib", "libmoe_latent.so")
 MOE_OK, MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE, MOE_EHIP, MOE_EINTERNAL = 0, -1, -2, -3, -4, -5
 MOE_OPND_BF16X2, MOE_OPND_BF16, MOE_OPND_MX8X3, MOE_OPND_MX6X3 = 0, 1, 2, 3
 MOE_OP_GATEUP_SITU, MOE_OP_DOWN, MOE_OP_GATEUP_SITU_BF16X2 = 0, 1, 2
-MOE_DT_F32, MOE_DT_BF16, MOE_DT_BF16X2 = 0, 1, 2
+MOE_DT_F32, MOE_DT_BF16, MOE_DT_BF16X2, MOE_DT_MXFP4 = 0, 1, 2, 3
 MOE_ROUTE_NOALLOC_SCRATCH_BYTES = 8 << 20
 (MOE_FN_ROUTE, MOE_FN_PERMUTE, MOE_FN_GROUPED_GEMM, MOE_FN_COMBINE_NORM_UP, MOE_FN_SHARED_FFN,
  MOE_FN_REAP_SALIENCY, MOE_FN_COMBINE_NORM_UP_REAP, MOE_FN_GROUPED_GEMM_TWO_BANK) = range(8)
 MOE_WF_MXFP4, MOE_WF_AFFINE2 = 0, 1
 MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_FULL = range(4)
 MOE_SCALE_F32, MOE_SCALE_E8M0 = 0, 1
+MOE_MX_SCALE_FIT, MOE_MX_SCALE_OCP = 0, 1
 MOE_FEW_MAX_T = 4
 
 EXPORTS = ("moe_abi_version", "moe_strerror", "moe_workspace_bytes", "moe_route", "moe_permute",
            "mxfp4_grouped_gemm", "moe_combine_norm_up", "shared_expert_ffn", "moe_reap_saliency",
            "moe_combine_norm_up_reap", "moe_route_capped", "moe_route_noalloc",
            "moe_grouped_gemm_two_bank", "moe_block_pre_norm", "moe_block_post_norm", "moe_fp8_quantize",
-           "moe_fp8_gemm_workspace_bytes", "moe_fp8_gemm", "moe_layer_few_workspace_bytes", "moe_layer_few")
+           "moe_fp8_gemm_workspace_bytes", "moe_fp8_gemm", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
+           "moe_mxfp4_gemm_workspace_bytes", "moe_mxfp4_gemm", "moe_mxfp4_expert_gemm_workspace_bytes",
+           "moe_mxfp4_expert_gemm", "moe_layer_few_workspace_bytes", "moe_layer_few")
 
 
 class MoeShape(ctypes.Structure):
@@ -63,6 +66,18 @@ class MoePostNormArgs(ctypes.Structure):
         ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("gate_kind", ctypes.c_int32),
         ("gate_dtype", ctypes.c_int32), ("gate_sigmoid", ctypes.c_int32), ("scale", ctypes.c_float),
         ("eps", ctypes.c_float), ("next", ctypes.POINTER(MoeNormOut)),
+    ]
+
+
+class MoeMxfp4ExpertArgs(ctypes.Structure):
+    _fields_ = [
+        ("n_experts", ctypes.c_int32), ("P", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("expert_offsets", ctypes.c_void_p), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+        ("x_scale", ctypes.c_void_p), ("ldxs", ctypes.c_int64), ("x_rows", ctypes.c_int32), ("top_k", ctypes.c_int32),
+        ("sorted_pair", ctypes.c_void_p), ("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p),
+        ("w3", ctypes.c_void_p), ("w3_scale", ctypes.c_void_p), ("beta", ctypes.c_float),
+        ("beta_lin", ctypes.c_float), ("pair_weight", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("ldo", ctypes.c_int64), ("out_dtype", ctypes.c_int32), ("out_scale", ctypes.c_void_p), ("ldos", ctypes.c_int64),
     ]
 
 
@@ -130,6 +145,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moe_fp8_gemm_workspace_bytes.argtypes = [i32, i32, i32]
     lib.moe_fp8_gemm.restype = i32
     lib.moe_fp8_gemm.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, vp, i32, vp, i32, i64, i32, vp, sz, vp]
+    lib.moe_mxfp4_quantize.restype = i32
+    lib.moe_mxfp4_quantize.argtypes = [i32, i32, vp, i32, i64, i32, vp, i64, vp, i64, vp]
+    lib.moe_mxfp4_dequantize.restype = i32
+    lib.moe_mxfp4_dequantize.argtypes = [i32, i32, vp, i64, vp, i64, vp, i32, i64, vp]
+    lib.moe_mxfp4_gemm_workspace_bytes.restype = sz
+    lib.moe_mxfp4_gemm_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.moe_mxfp4_gemm.restype = i32
+    lib.moe_mxfp4_gemm.argtypes = [i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, i32, i64, i32, vp, sz, vp]
+    lib.moe_mxfp4_expert_gemm_workspace_bytes.restype = sz
+    lib.moe_mxfp4_expert_gemm_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.moe_mxfp4_expert_gemm.restype = i32
+    lib.moe_mxfp4_expert_gemm.argtypes = [ctypes.POINTER(MoeMxfp4ExpertArgs), vp, sz, vp]
     lib.moe_layer_few_workspace_bytes.restype = sz
     lib.moe_layer_few_workspace_bytes.argtypes = [sp, i32]
     lib.moe_layer_few.restype = i32

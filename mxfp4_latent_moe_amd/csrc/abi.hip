@@ -530,6 +530,142 @@ static int fp8_gemm_impl(int T, int N, int K, const uint8_t *x, int64_t ldx, con
                          static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
+// ---- MXFP4 rows and products with both operands in MXFP4
+
+// rows of codes whose chunks of 8 values (4 bytes) are whole and can be moved as one
+static bool chunked4(const void *q, long long ldq) { return aligned(q, 4) && ldq % 4 == 0; }
+
+static int mxfp4_quantize_impl(int T, int K, const void *x, int x_dtype, int64_t ldx, int scale_rule, uint8_t *q,
+                               int64_t ldq, uint8_t *q_scale, int64_t ldqs, void *stream) {
+  if (T < 0 || K <= 0 || !x || !q || !q_scale || !is_float_dtype(x_dtype)) return MOE_EINVAL;
+  if (scale_rule != MOE_MX_SCALE_FIT && scale_rule != MOE_MX_SCALE_OCP) return MOE_EINVAL;
+  if (ldx < K || ldq < (K - 1) / 2 + 1 || ldqs < (K - 1) / 32 + 1 || !aligned(x, dtype_bytes(x_dtype))) return MOE_EINVAL;
+  if (K > QUANT_MAX_K) return MOE_ENOTSUP;
+  const int rc = check_device();
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  const bool vec = K % 8 == 0 && chunked(x, ldx, dtype_bytes(x_dtype)) && chunked4(q, ldq);
+  return launch_quantize4(x, x_dtype == MOE_DT_BF16, ldx, T, K, vec, scale_rule == MOE_MX_SCALE_OCP, q, ldq, q_scale,
+                          ldqs, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+static int mxfp4_dequantize_impl(int T, int K, const uint8_t *q, int64_t ldq, const uint8_t *q_scale, int64_t ldqs,
+                                 void *out, int out_dtype, int64_t ldo, void *stream) {
+  if (T < 0 || K <= 0 || !out || !q || !q_scale || !is_float_dtype(out_dtype)) return MOE_EINVAL;
+  if (ldo < K || ldq < (K - 1) / 2 + 1 || ldqs < (K - 1) / 32 + 1 || !aligned(out, dtype_bytes(out_dtype)))
+    return MOE_EINVAL;
+  if (K > QUANT_MAX_K) return MOE_ENOTSUP;
+  const int rc = check_device();
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  const bool vec = K % 8 == 0 && chunked(out, ldo, dtype_bytes(out_dtype)) && chunked4(q, ldq);
+  return launch_dequantize4(q, ldq, q_scale, ldqs, T, K, vec, out, out_dtype == MOE_DT_BF16, ldo,
+                            static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+// limits of the products' kernels: whole blocks, 32-bit offsets within the rows
+// one work-group reads, and a count of work items in 32 bits
+static int mxfp4_check_sizes(int P, int N, int K) {
+  if (P < 0 || N <= 0 || K <= 0) return MOE_EINVAL;
+  if (K % 32 || K > (1 << 20) || P > (1 << 21) || N > (1 << 20)) return MOE_ENOTSUP;
+  return MOE_OK;
+}
+static bool rows_vec(const void *p, long long ld, int dtype) {
+  const size_t piece = dtype == MOE_DT_BF16 ? 8 : 16;
+  return aligned(p, piece) && (ld * (long long)dtype_bytes(dtype)) % (long long)piece == 0;
+}
+
+static int mxfp4_gemm_impl(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8_t *x_scale, int64_t ldxs,
+                           const uint8_t *w, const uint8_t *w_scale, void *out, int out_dtype, int64_t ldo,
+                           int accumulate, void *ws, size_t ws_bytes, void *stream) {
+  int rc = mxfp4_check_sizes(T, N, K);
+  if (rc) return rc;
+  if (!x || !x_scale || !w || !w_scale || !out || !ws || !is_float_dtype(out_dtype)) return MOE_EINVAL;
+  if (accumulate != 0 && (accumulate != 1 || out_dtype != MOE_DT_F32)) return MOE_EINVAL;
+  if (ldx < K / 2 || ldxs < K / 32 || ldo < N) return MOE_EINVAL;
+  if (!aligned16(x) || ldx % 16 || !aligned16(w) || !aligned16(ws) || !aligned(out, dtype_bytes(out_dtype)))
+    return MOE_EINVAL;
+  if (ldx > (1 << 22) || ldxs > (1 << 22)) return MOE_ENOTSUP;
+  if (ws_bytes < moe_mxfp4_gemm_workspace_bytes(T, N, K)) return MOE_EWORKSPACE;
+  if ((rc = check_device())) return rc;
+  if (T == 0) return MOE_OK;
+  Mx4Args g{};
+  g.x = x;
+  g.ldx = ldx;
+  g.sx = x_scale;
+  g.ldsx = ldxs;
+  g.x_rows = T;
+  g.w[0] = w;
+  g.sw[0] = w_scale;
+  g.out = out;
+  g.ldo = ldo;
+  g.out_kind = out_dtype == MOE_DT_BF16 ? MX4_OUT_BF16 : MX4_OUT_F32;
+  g.accumulate = accumulate;
+  g.vec_out = rows_vec(out, ldo, out_dtype);
+  g.P = T;
+  g.N = N;
+  g.K = K;
+  return launch_mx4_gemm(g, ws, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+static int mxfp4_expert_impl(const moe_mxfp4_expert_args *a, void *ws, size_t ws_bytes, void *stream) {
+  if (!a || a->n_experts <= 0) return MOE_EINVAL;
+  const int P = a->P, N = a->N, K = a->K;
+  int rc = mxfp4_check_sizes(P, N, K);
+  if (rc) return rc;
+  const bool pair = a->w3 != nullptr, four = a->out_dtype == MOE_DT_MXFP4;
+  if (!a->expert_offsets || !a->x || !a->x_scale || !a->w || !a->w_scale || !a->out || !ws) return MOE_EINVAL;
+  if (pair != (a->w3_scale != nullptr) || (!four && !is_float_dtype(a->out_dtype))) return MOE_EINVAL;
+  if (pair && (a->pair_weight || !(a->beta > 0.f) || !(a->beta_lin > 0.f))) return MOE_EINVAL;
+  if (four != (a->out_scale != nullptr) || (four && !pair)) return MOE_EINVAL;
+  const bool gathered = a->top_k != 0;
+  if (a->top_k < 0 || ((gathered || a->pair_weight) && !a->sorted_pair)) return MOE_EINVAL;
+  if (a->x_rows < (gathered ? 1 : P)) return MOE_EINVAL;
+  if (a->ldx < K / 2 || a->ldxs < K / 32) return MOE_EINVAL;
+  if (!aligned16(a->x) || a->ldx % 16 || !aligned16(a->w) || !aligned16(a->w3) || !aligned16(ws)) return MOE_EINVAL;
+  if (!aligned(a->expert_offsets, 4) || !aligned(a->sorted_pair, 4) || !aligned(a->pair_weight, 4)) return MOE_EINVAL;
+  if (four) {
+    if (N % 32) return MOE_ENOTSUP;
+    if (a->ldo < N / 2 || a->ldo % 16 || !aligned16(a->out) || a->ldos < N / 32) return MOE_EINVAL;
+  } else if (a->ldo < N || !aligned(a->out, dtype_bytes(a->out_dtype))) {
+    return MOE_EINVAL;
+  }
+  if (a->n_experts > MX4_MAX_E || a->ldx > (1 << 22) || a->ldxs > (1 << 22)) return MOE_ENOTSUP;
+  // gathered rows are addressed with 32 bits from the first one
+  if (gathered && (long long)a->x_rows * a->ldx >= (1LL << 31)) return MOE_ENOTSUP;
+  if (gathered && (long long)a->x_rows * a->ldxs >= (1LL << 31)) return MOE_ENOTSUP;
+  if (ws_bytes < moe_mxfp4_expert_gemm_workspace_bytes(a->n_experts, P, N, K)) return MOE_EWORKSPACE;
+  if ((rc = check_device())) return rc;
+  if (P == 0) return MOE_OK;
+  Mx4Args g{};
+  g.x = a->x;
+  g.ldx = a->ldx;
+  g.sx = a->x_scale;
+  g.ldsx = a->ldxs;
+  g.x_rows = a->x_rows;
+  g.map = gathered ? a->sorted_pair : nullptr;
+  g.div = a->top_k;
+  g.w[0] = a->w;
+  g.w[1] = a->w3;
+  g.sw[0] = a->w_scale;
+  g.sw[1] = a->w3_scale;
+  g.beta = a->beta;
+  g.beta_lin = a->beta_lin;
+  g.pair_weight = a->pair_weight;
+  g.pair = a->sorted_pair;
+  g.out = a->out;
+  g.ldo = a->ldo;
+  g.os = a->out_scale;
+  g.ldos = a->ldos;
+  g.out_kind = four ? MX4_OUT_MX4 : a->out_dtype == MOE_DT_BF16 ? MX4_OUT_BF16 : MX4_OUT_F32;
+  g.vec_out = !four && rows_vec(a->out, a->ldo, a->out_dtype);
+  g.P = P;
+  g.N = N;
+  g.K = K;
+  return launch_mx4_expert(g, a->expert_offsets, a->n_experts, ws, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? MOE_OK : MOE_EHIP;
+}
+
 // ---- the layer for a few tokens
 struct FewWs {
   size_t list, wts, logits, ss, sd, y, z, hs, h, yn, total;
@@ -1169,6 +1305,41 @@ int moe_fp8_gemm(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8
     return fp8_gemm_impl(T, N, K, x, ldx, x_scale, ldxs, w, w_scale, w_scale_type, out, out_dtype, ldo, accumulate,
                          ws, ws_bytes, stream);
   });
+}
+
+int moe_mxfp4_quantize(int T, int K, const void *x, int x_dtype, int64_t ldx, int scale_rule, uint8_t *q, int64_t ldq,
+                       uint8_t *q_scale, int64_t ldqs, void *stream) {
+  return guarded(
+      [&]() -> int { return mxfp4_quantize_impl(T, K, x, x_dtype, ldx, scale_rule, q, ldq, q_scale, ldqs, stream); });
+}
+
+int moe_mxfp4_dequantize(int T, int K, const uint8_t *q, int64_t ldq, const uint8_t *q_scale, int64_t ldqs, void *out,
+                         int out_dtype, int64_t ldo, void *stream) {
+  return guarded(
+      [&]() -> int { return mxfp4_dequantize_impl(T, K, q, ldq, q_scale, ldqs, out, out_dtype, ldo, stream); });
+}
+
+size_t moe_mxfp4_gemm_workspace_bytes(int T, int N, int K) {
+  if (mxfp4_check_sizes(T, N, K) != MOE_OK) return 0;
+  return ALIGN + align_up(mx4_workspace_bytes(T, N, K));
+}
+
+int moe_mxfp4_gemm(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8_t *x_scale, int64_t ldxs,
+                   const uint8_t *w, const uint8_t *w_scale, void *out, int out_dtype, int64_t ldo, int accumulate,
+                   void *ws, size_t ws_bytes, void *stream) {
+  return guarded([&]() -> int {
+    return mxfp4_gemm_impl(T, N, K, x, ldx, x_scale, ldxs, w, w_scale, out, out_dtype, ldo, accumulate, ws, ws_bytes,
+                           stream);
+  });
+}
+
+size_t moe_mxfp4_expert_gemm_workspace_bytes(int E, int P, int N, int K) {
+  if (E <= 0 || E > MX4_MAX_E || mxfp4_check_sizes(P, N, K) != MOE_OK) return 0;
+  return ALIGN + align_up(mx4_expert_workspace_bytes(E, P, N, K));
+}
+
+int moe_mxfp4_expert_gemm(const moe_mxfp4_expert_args *a, void *ws, size_t ws_bytes, void *stream) {
+  return guarded([&]() -> int { return mxfp4_expert_impl(a, ws, ws_bytes, stream); });
 }
 
 size_t moe_layer_few_workspace_bytes(const moe_shape *s, int T) {

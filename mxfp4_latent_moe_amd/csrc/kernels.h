@@ -229,6 +229,41 @@ struct Fp8Args {
 size_t fp8_workspace_bytes(int T, int N, int K);
 hipError_t launch_fp8_gemm(const Fp8Args &g, bool e8, bool out_bf16, void *ws, hipStream_t st);
 
+// ---- MXFP4 rows, and products with both operands in MXFP4
+enum { MX4_OUT_F32 = 0, MX4_OUT_BF16 = 1, MX4_OUT_MX4 = 2 };
+struct Mx4Args {
+  const uint8_t *x;       // codes, ldx bytes a row
+  long long ldx;
+  const uint8_t *sx;      // scale bytes
+  long long ldsx;
+  int x_rows;
+  const int32_t *map;     // row p of the product reads row map[p] / div of x (NULL: row p)
+  int div;
+  const uint8_t *w[2];    // codes [E][N][K / 2]; w[1] != NULL: SiTU-GLU of the two products
+  const uint8_t *sw[2];   // scale bytes [E][N][K / 32]
+  float beta, beta_lin;
+  const float *pair_weight;  // row p is scaled by pair_weight[pair[p]] (NULL: not)
+  const int32_t *pair;
+  void *out;              // ldo elements (MX4_OUT_MX4: bytes) a row
+  long long ldo;
+  uint8_t *os;            // MX4_OUT_MX4: scale bytes
+  long long ldos;
+  int out_kind, accumulate;
+  int vec_out;            // rows of out are 16-byte (bf16: 8-byte) aligned
+  int P, N, K;
+  const int4 *chunks;     // grouped: {expert, first row, rows, 0} and their number (NULL: dense)
+  const int32_t *chunk_count;
+};
+constexpr int MX4_MAX_E = 1024;  // experts of a grouped call
+hipError_t launch_quantize4(const void *x, bool x_bf16, long long ldx, int T, int K, bool vec, bool ocp, uint8_t *q,
+                            long long ldq, uint8_t *qs, long long ldqs, hipStream_t st);
+hipError_t launch_dequantize4(const uint8_t *q, long long ldq, const uint8_t *qs, long long ldqs, int T, int K, bool vec,
+                              void *out, bool out_bf16, long long ldo, hipStream_t st);
+size_t mx4_workspace_bytes(int T, int N, int K);
+hipError_t launch_mx4_gemm(const Mx4Args &g, void *ws, hipStream_t st);
+size_t mx4_expert_workspace_bytes(int E, int P, int N, int K);
+hipError_t launch_mx4_expert(const Mx4Args &g, const int32_t *offsets, int E, void *ws, hipStream_t st);
+
 // ---- the layer for a few tokens
 constexpr int FEW_MAX_T = 4;
 constexpr int FEW_MAX_PAIRS = FEW_MAX_T * 32;  // (token, expert) pairs

@@ -280,6 +280,112 @@ def fp8_gemm(x, x_scale, w, w_scale, out, ws, accumulate=False, stream=None):
              _FLOATS[out.dtype], ldo, int(accumulate), _p(ws), _bytes("ws", ws, dev))
 
 
+_PACKED = tuple(d for d in (torch.uint8, getattr(torch, "float4_e2m1fn_x2", None)) if d is not None)
+_RULES = {"fit": _lib.MOE_MX_SCALE_FIT, "ocp": _lib.MOE_MX_SCALE_OCP}
+
+
+def mxfp4_quantize(x, q, q_scale, rule="fit", stream=None):
+    """Rows of x [T, K] (fp32 or bf16) in MXFP4 (moe_mxfp4_quantize): e2m1 codes q [T, ceil(K / 2)], element 2b in
+    byte b's low nibble, and scale bytes q_scale [T, ceil(K / 32)].  rule "fit": the smallest power-of-two scale with
+    which nothing saturates; "ocp": the MX format's own, by the largest magnitude's exponent."""
+    T, K = x.shape
+    if rule not in _RULES:
+        raise ValueError(f"rule: {rule!r}, want one of {tuple(_RULES)}")
+    ldx = _rows("x", x, (T, K), _FLOATS, x.device)
+    ldq = _rows("q", q, (T, -(-K // 2)), _PACKED, x.device)
+    lds = _rows("q_scale", q_scale, (T, -(-K // 32)), _SCALES, x.device)
+    if T == 0:
+        return
+    _enqueue("moe_mxfp4_quantize", x.device, stream, T, K, _p(x), _FLOATS[x.dtype], ldx, _RULES[rule], _p(q), ldq,
+             _p(q_scale), lds)
+
+
+def mxfp4_dequantize(q, q_scale, out, stream=None):
+    """MXFP4 rows (see mxfp4_quantize) as values: out [T, K] fp32 or bf16 (moe_mxfp4_dequantize)."""
+    T, K = out.shape
+    ldq = _rows("q", q, (T, -(-K // 2)), _PACKED, out.device)
+    lds = _rows("q_scale", q_scale, (T, -(-K // 32)), _SCALES, out.device)
+    ldo = _rows("out", out, (T, K), _FLOATS, out.device)
+    if T == 0:
+        return
+    _enqueue("moe_mxfp4_dequantize", out.device, stream, T, K, _p(q), ldq, _p(q_scale), lds, _p(out),
+             _FLOATS[out.dtype], ldo)
+
+
+def mxfp4_gemm_workspace_bytes(T: int, N: int, K: int) -> int:
+    return int(load().moe_mxfp4_gemm_workspace_bytes(T, N, K))
+
+
+def _stack(name, t, shape, dtypes, device):
+    """The pointer of a contiguous weight tensor, after its checks."""
+    if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, want contiguous {shape} on {device}, "
+                         f"one of {dtypes}")
+    return t.data_ptr()
+
+
+def mxfp4_gemm(x, x_scale, w, w_scale, out, ws, accumulate=False, stream=None):
+    """out [T, N] (+)= x w^T with both operands in MXFP4 (moe_mxfp4_gemm): x [T, K / 2] with scale bytes [T, K / 32]
+    (see mxfp4_quantize), w [N, K / 2] with w_scale [N, K / 32].  out is fp32 or bf16; ws holds
+    mxfp4_gemm_workspace_bytes(T, N, K) bytes."""
+    (T, N), K, dev = out.shape, 2 * w.shape[-1], w.device
+    ldx = _rows("x", x, (T, K // 2), _PACKED, dev)
+    lds = _rows("x_scale", x_scale, (T, K // 32), _SCALES, dev)
+    pw, pws = _stack("w", w, (N, K // 2), _PACKED, dev), _stack("w_scale", w_scale, (N, K // 32), _SCALES, dev)
+    ldo = _rows("out", out, (T, N), _FLOATS, dev)
+    if T == 0:
+        return
+    _enqueue("moe_mxfp4_gemm", dev, stream, T, N, K, _p(x), ldx, _p(x_scale), lds, pw, pws, _p(out),
+             _FLOATS[out.dtype], ldo, int(accumulate), _p(ws), _bytes("ws", ws, dev))
+
+
+def mxfp4_expert_gemm_workspace_bytes(E: int, P: int, N: int, K: int) -> int:
+    return int(load().moe_mxfp4_expert_gemm_workspace_bytes(E, P, N, K))
+
+
+def mxfp4_expert_gemm(x, x_scale, w, w_scale, offsets, out, ws, w3=None, w3_scale=None, sorted_pair=None, top_k=0,
+                      pair_weight=None, beta=4.0, beta_lin=25.0, out_scale=None, stream=None):
+    """The routed experts' products on MXFP4 rows (moe_mxfp4_expert_gemm): out [P, N], rows sorted by expert, expert e
+    owning rows offsets[e] .. offsets[e + 1] (int32 [E + 1]; rows from offsets[E] on are left as they were).
+    x [rows, K / 2] with x_scale [rows, K / 32]: row p itself, or with top_k row sorted_pair[p] // top_k.
+    w [E, N, K / 2] with w_scale [E, N, K / 32]; with w3 and w3_scale the result is SiTU-GLU of the two products.
+    pair_weight (fp32, without w3): row p times pair_weight[sorted_pair[p]].  out is fp32, bf16, or with w3 MXFP4:
+    codes [P, N / 2] with out_scale [P, N / 32].  ws holds mxfp4_expert_gemm_workspace_bytes(E, P, N, K) bytes."""
+    dev = w.device
+    if w.dim() != 3:
+        raise ValueError(f"w: shape {tuple(w.shape)}, want [E, N, K / 2]")
+    E, N, K = w.shape[0], w.shape[1], 2 * w.shape[2]
+    P = out.shape[0]
+    a = _lib.MoeMxfp4ExpertArgs()
+    a.n_experts, a.P, a.N, a.K, a.top_k, a.x_rows = E, P, N, K, top_k, x.shape[0]
+    a.beta, a.beta_lin = beta, beta_lin
+    a.x, a.ldx = _p(x), _rows("x", x, (x.shape[0], K // 2), _PACKED, dev)
+    a.x_scale, a.ldxs = _p(x_scale), _rows("x_scale", x_scale, (x.shape[0], K // 32), _SCALES, dev)
+    a.w, a.w_scale = _stack("w", w, (E, N, K // 2), _PACKED, dev), _stack("w_scale", w_scale, (E, N, K // 32), _SCALES, dev)
+    if (w3 is None) != (w3_scale is None):
+        raise ValueError("w3 and w3_scale go together")
+    if w3 is not None:
+        a.w3 = _stack("w3", w3, (E, N, K // 2), _PACKED, dev)
+        a.w3_scale = _stack("w3_scale", w3_scale, (E, N, K // 32), _SCALES, dev)
+    a.expert_offsets = _vector("offsets", offsets, E + 1, torch.int32, dev)
+    if sorted_pair is not None:
+        a.sorted_pair = _vector("sorted_pair", sorted_pair, P, torch.int32, dev)
+    if pair_weight is not None:
+        if pair_weight.dtype != torch.float32 or pair_weight.device != dev or not pair_weight.is_contiguous():
+            raise ValueError(f"pair_weight: want contiguous float32 on {dev}")
+        a.pair_weight = _p(pair_weight)
+    if out_scale is not None:
+        a.out_dtype, a.ldo = _lib.MOE_DT_MXFP4, _rows("out", out, (P, N // 2), _PACKED, dev)
+        a.out_scale, a.ldos = _p(out_scale), _rows("out_scale", out_scale, (P, N // 32), _SCALES, dev)
+    else:
+        a.ldo = _rows("out", out, (P, N), _FLOATS, dev)
+        a.out_dtype = _FLOATS[out.dtype]
+    a.out = _p(out)
+    if P == 0:
+        return
+    _enqueue("moe_mxfp4_expert_gemm", dev, stream, a, _p(ws), _bytes("ws", ws, dev))
+
+
 def layer_weights(weights: dict) -> _lib.MoeLayerWeights:
     """moe_layer_weights of a LatentMoE weight dict (which must stay alive)."""
     lw = _lib.MoeLayerWeights()

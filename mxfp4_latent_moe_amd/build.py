@@ -28,7 +28,7 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["abi.hip", "gemm.hip", "stream.hip", "grouped_stream.hip", "prefill.hip", "route.hip",
            "permute.hip", "combine.hip", "mx8.hip", "dense.hip", "reap.hip", "prefill_pl.hip",
            "block.hip", "fp8.hip", "few.hip", "mx4.hip"]
-CHECKED = ["dense.hip", "fp8.hip", "prefill.hip", "prefill_pl.hip"]  # issue LDS reads in inline assembly
+CHECKED = ["dense.hip", "fp8.hip", "mx4.hip", "prefill.hip", "prefill_pl.hip"]  # issue LDS reads in inline assembly
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -153,8 +153,9 @@ struct Chunk {
   int expert, row, n;
 };
 
-// Chunks of at most `rows` sorted rows, an expert's one after the other.  Bad
-// offsets give wrong chunks but none outside the P rows and the list's `cap`.
+// Chunks of at most `rows` sorted rows, an expert's one after the other and, in
+// whole tiles of 32, of one size.  Bad offsets give wrong chunks but none outside
+// the P rows and the list's `cap`.
 __global__ __launch_bounds__(1024) void mx4_plan_kernel(const int32_t *offsets, int E, int P, int rows, int cap,
                                                         int4 *chunks, int32_t *count) {
   __shared__ int tot[16];
@@ -178,8 +179,9 @@ __global__ __launch_bounds__(1024) void mx4_plan_kernel(const int32_t *offsets, 
     if (w < wave) at += tot[w];
     sum += tot[w];
   }
+  const int each = nch > 0 ? ((ne + nch - 1) / nch + 31) / 32 * 32 : 0;
   for (int i = 0; i < nch && at + i < cap; ++i)
-    chunks[at + i] = int4{e, lo + i * rows, min(rows, ne - i * rows), 0};
+    chunks[at + i] = int4{e, lo + i * each, min(each, ne - i * each), 0};
   if (e == 0) *count = min(sum, cap);
 }
 
@@ -350,6 +352,398 @@ __global__ __launch_bounds__(64 * NW) void mx4_stream_kernel(Mx4Args g) {
   }
 }
 
+// ---- many rows
+// A work-group of four waves, one a SIMD, owns 256 weight rows (of a pair, 128 of
+// each matrix) and up to 256 rows of x; a wave of it 64 weight rows and all of
+// the rows, 2 x NT tiles of 32 x 32.  Both operands pass through ST LDS stages of
+// 256 inputs, filled by direct loads of rows' whole 128 bytes between the products.
+//
+// A row's 128 bytes are eight pieces of 16, a block of 32 codes each; piece p of
+// row r lies at position p ^ (r / 2 % 8), so the 16 rows that a quarter wave reads
+// at once, two to a 256-byte line of LDS, fall on different banks.  Product j of a
+// stage takes piece 4 h + j from the lanes of half h: the two halves of the
+// instruction's K need not be neighbours in memory, and the four scale bytes that
+// a lane needs in a stage are then one dword, from which the instruction selects
+// byte j.  Scales come into LDS 16 bytes a row, two stages at a time.
+//
+// SG: scale rows are whole dwords apart and aligned, so that those 16 bytes can be
+// loaded directly; else they come byte by byte through registers.
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// 16 bytes of LDS at a + O, issued without waiting
+template <int O>
+MOE_DEV void tread(uint32_t a, u32x4_t &v) {
+  static_assert(O >= 0 && O < 65536, "offset field");
+  asm volatile("ds_read_b128 %0, %1 offset:%2" : "=&v"(v) : "v"(a), "n"(O) : "memory");
+}
+template <int O>
+MOE_DEV void tread4(uint32_t a, uint32_t &v) {
+  static_assert(O >= 0 && O < 65536, "offset field");
+  asm volatile("ds_read_b32 %0, %1 offset:%2" : "=&v"(v) : "v"(a), "n"(O) : "memory");
+}
+template <int N>
+MOE_DEV void twait() {
+  asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(N < 15 ? N : 15) : "memory");
+}
+// ties a register to the wait before: its users stay behind it
+template <typename V>
+MOE_DEV void ttie(V &v) {
+  asm volatile("" : "+v"(v));
+}
+
+// c + 32 rows times 32 columns over 64 codes, scaled by byte J of each operand's scales
+template <int J>
+MOE_DEV f32x16_t mfma_4_32(u32x4_t w, u32x4_t x, f32x16_t c, uint32_t sw, uint32_t sx) {
+  const i32x4_t w4 = __builtin_bit_cast(i32x4_t, w), x4 = __builtin_bit_cast(i32x4_t, x);
+  const i32x8_t a = __builtin_shufflevector(w4, w4, 0, 1, 2, 3, -1, -1, -1, -1);
+  const i32x8_t b = __builtin_shufflevector(x4, x4, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, J, (int)sw, J, (int)sx);
+}
+
+constexpr int TILE_ROWS = 256;    // rows of x
+constexpr int TILE_COLS = 256;    // weight rows
+constexpr int stages_of(int nt) { return nt == 1 ? 4 : nt <= 4 ? 3 : 2; }
+constexpr int stage_bytes(int nt) { return (TILE_COLS + 32 * nt) * 128; }
+constexpr int GROUP_BYTES = (TILE_COLS + TILE_ROWS) * 16;  // scales of two stages
+constexpr int tile_lds(int nt) { return stages_of(nt) * stage_bytes(nt) + 2 * GROUP_BYTES; }
+constexpr int max_lds(int nt) { return nt == 0 ? 0 : tile_lds(nt) > max_lds(nt - 1) ? tile_lds(nt) : max_lds(nt - 1); }
+constexpr int TILE_LDS = max_lds(8);
+static_assert(TILE_LDS <= 160 * 1024, "LDS of a CU");
+
+// rows c of x times weight rows of columns n0 .., stages first .. first + count - 1 of K (first even)
+template <int NT, bool PAIR, bool SG>
+MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int count, float *partial, uint8_t *lds) {
+  constexpr int ST = stages_of(NT), SB = stage_bytes(NT), GB = GROUP_BYTES;
+  constexpr int WL = 8, XL = NT;  // direct loads of a wave per stage, 8 rows each
+  const int tid = threadIdx.x, lane = tid & 63, r32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kbytes = g.K / 2, kb = g.K / 32;
+  const int ncols = min(PAIR ? TILE_COLS / 2 : TILE_COLS, g.N - n0);
+  uint8_t *const groups = lds + ST * SB;
+
+  // columns and rows past the end are out of range: zeros
+  __amdgpu_buffer_rsrc_t wr[PAIR ? 2 : 1], sr[PAIR ? 2 : 1];
+#pragma unroll
+  for (int m = 0; m < (PAIR ? 2 : 1); ++m) {
+    const long long row = (long long)c.expert * g.N + n0;
+    wr[m] = make_rsrc(g.w[m] + row * kbytes, (uint32_t)ncols * (uint32_t)kbytes);
+    sr[m] = make_rsrc(g.sw[m] + row * kb, (uint32_t)ncols * (uint32_t)kb);
+  }
+  const long long base = g.map != nullptr ? 0 : c.row;
+  const int xrows = g.map != nullptr ? g.x_rows : c.n;
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + base * g.ldx, (uint32_t)((xrows - 1) * g.ldx + kbytes));
+  const __amdgpu_buffer_rsrc_t xsr = make_rsrc(g.sx + base * g.ldsx, (uint32_t)((xrows - 1) * g.ldsx + kb));
+  constexpr uint32_t OUT = 0x80000000u;  // past the end of every buffer
+  auto row_of = [&](int r) { return (uint32_t)(x_row(g, c.row + r) - (int)base); };
+
+  // direct load u of this wave fills 8 rows of a stage: lane i's 16 bytes land at
+  // position i % 8 of row i / 8
+  const int l8 = lane >> 3;
+  uint32_t piece[2], vw[WL], vx[XL];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) piece[q] = 16 * ((lane & 7) ^ (4 * q + (lane >> 4)));
+#pragma unroll
+  for (int u = 0; u < WL; ++u) {
+    const int n = PAIR ? 32 * wave + 8 * (u & 3) + l8 : 64 * wave + 8 * u + l8;
+    vw[u] = (uint32_t)n * (uint32_t)kbytes + piece[u & 1];
+  }
+#pragma unroll
+  for (int u = 0; u < XL; ++u) {
+    const int r = 8 * (4 * u + wave) + l8;
+    vx[u] = r < c.n ? row_of(r) * (uint32_t)g.ldx + piece[wave & 1] : OUT;
+  }
+  auto past = [&](int b, uint32_t p) {  // of a stage that ends inside, or after the last
+    return b < count && 128u * (first + b) + p < (uint32_t)kbytes ? 0u : OUT;
+  };
+  // load u of stage b, to the place at `place` of the ring
+  auto request = [&](uint32_t place, int b, const uint32_t (&out)[2], auto uc) {
+    constexpr int u = decltype(uc)::value;
+    uint8_t *const at = lds + place;
+    const uint32_t k0 = 128u * (first + b);
+    if constexpr (u < WL)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[PAIR && u >= 4 ? 1 : 0], (lds_void *)(at + (64 * wave + 8 * u) * 128), 16,
+                                               vw[u] | out[u & 1], k0, 0, 0);
+    else if constexpr (u < WL + XL)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          xr, (lds_void *)(at + (TILE_COLS + 8 * (4 * (u - WL) + wave)) * 128), 16, vx[u - WL] | out[wave & 1], k0, 0, 0);
+  };
+  // scales of stages 2 q and 2 q + 1: [row][16]; of a pair first one matrix's 128 rows, then the other's
+  const int sn = PAIR ? 64 * (wave & 1) + lane : 64 * wave + lane, st = 64 * wave + lane;
+  const uint32_t vs = (uint32_t)sn * (uint32_t)kb;
+  const uint32_t vt = st < c.n ? row_of(st) * (uint32_t)g.ldsx : OUT;
+  u32x4_t held[2];  // without SG: on their way through registers
+  auto request_scales = [&](int q) {
+    const uint32_t at = 16u * (first / 2 + q);
+    if constexpr (SG) {
+      uint8_t *const to = groups + (q & 1) * GB;
+      const uint32_t none = 2 * q < count ? 0u : OUT;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(sr[PAIR ? wave >> 1 : 0], (lds_void *)(to + 1024 * wave), 16, vs | none, at, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xsr, (lds_void *)(to + TILE_COLS * 16 + 1024 * wave), 16, vt | none, at, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t none = at + i < (uint32_t)kb ? 0u : OUT;
+        const uint32_t a = __builtin_amdgcn_raw_buffer_load_b8(sr[PAIR ? wave >> 1 : 0], vs | none, at + i, 0);
+        const uint32_t b = __builtin_amdgcn_raw_buffer_load_b8(xsr, vt | none, at + i, 0);
+        held[0][i >> 2] = i & 3 ? held[0][i >> 2] | a << (8 * (i & 3)) : a;
+        held[1][i >> 2] = i & 3 ? held[1][i >> 2] | b << (8 * (i & 3)) : b;
+      }
+    }
+  };
+  auto put_scales = [&](int q) {
+    if constexpr (!SG) {
+      u32x4_t *const to = reinterpret_cast<u32x4_t *>(groups + (q & 1) * GB);
+      to[tid] = held[0];
+      to[TILE_COLS + tid] = held[1];
+    }
+  };
+
+  f32x16_t acc[2][NT];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[m][i][r] = 0.f;
+  uint32_t frag[4];  // this lane's piece of row r32 for product j
+#pragma unroll
+  for (int j = 0; j < 4; ++j) frag[j] = lds_addr(lds) + 128 * r32 + 16 * ((4 * h + j) ^ (r32 >> 1 & 7));
+  const uint32_t sfrag = lds_addr(groups) + 16 * r32 + 4 * h;
+
+  request_scales(0);
+  put_scales(0);
+  static_for<ST - 1>([&](auto sc) {
+    constexpr int s = decltype(sc)::value;
+    const uint32_t out[2] = {past(s, piece[0]), past(s, piece[1])};
+    static_for<WL + XL>([&](auto uc) { request(s * SB, s, out, uc); });
+  });
+  // the order of a stage's LDS reads: the scales, the first product's weights and D
+  // rows' pieces; then with each tile the rows' piece D tiles on, and with a
+  // product's first tile the next product's weights
+  constexpr int F = 4 * NT, D = NT == 1 ? 2 : 3;
+  uint32_t place = 0;  // of this stage in the ring
+  auto step = [&](auto oddc, int b) {
+    constexpr bool odd = decltype(oddc)::value;
+    // this stage has landed (what was requested since is the next ones), and every
+    // wave is done with the one before, whose place is filled below
+    if constexpr (!SG) twait<0>();
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm((WL + XL) * (ST - 2)));
+    __builtin_amdgcn_s_barrier();
+    if constexpr (odd) put_scales(b / 2 + 1);
+    else request_scales(b / 2 + 1);
+    u32x4_t w[2][2], x[D + 1];
+    uint32_t sw[2], sx[NT];
+    const uint32_t sa = sfrag + (b / 2 & 1) * GB + (odd ? 8 : 0);
+    const uint32_t swa = sa + (PAIR ? 512 : 1024) * wave;
+    uint32_t fx[4], fw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      fx[j] = frag[j] + place;
+      fw[j] = fx[j] + 8192 * wave;
+    }
+    auto read_w = [&](auto jc) {
+      constexpr int j = decltype(jc)::value;
+      tread<0>(fw[j], w[j & 1][0]);
+      tread<4096>(fw[j], w[j & 1][1]);
+    };
+    auto read_x = [&](auto fc) {
+      constexpr int f = decltype(fc)::value;
+      tread<TILE_COLS * 128 + 4096 * (f % NT)>(fx[f / NT], x[f % (D + 1)]);
+    };
+    tread4<0>(swa, sw[0]);
+    tread4<PAIR ? 2048 : 512>(swa, sw[1]);
+    static_for<NT>([&](auto ic) { tread4<TILE_COLS * 16 + 512 * decltype(ic)::value>(sa, sx[decltype(ic)::value]); });
+    read_w(std::integral_constant<int, 0>{});
+    static_for<D>([&](auto fc) { read_x(fc); });
+    const uint32_t out[2] = {past(b + ST - 1, piece[0]), past(b + ST - 1, piece[1])};
+    const uint32_t next = place == 0 ? (ST - 1) * SB : place - SB;  // the place that stage b - 1 had
+    // scale bytes past K are of other rows: one in their place
+    const int in = kb - 8 * (first + b) - 4 * h;
+    const uint32_t mask = in >= 4 ? 0xFFFFFFFFu : in <= 0 ? 0u : (1u << (8 * in)) - 1u;
+    static_for<F>([&](auto fc) {
+      constexpr int f = decltype(fc)::value, j = f / NT, i = f % NT;
+      if constexpr (f + D < F) read_x(std::integral_constant<int, f + D>{});
+      if constexpr (i == 0 && j < 3) read_w(std::integral_constant<int, j + 1>{});
+      // reads behind the last one that this tile needs: rows' piece f (issued with
+      // tile f - D), and at a product's first tile the weights issued with the last
+      // product's first; weights are two reads
+      constexpr int from = f < D ? 0 : f - D + 1;          // tiles since piece f went out, this one among them
+      constexpr int xs_behind = (f + D < F ? f + D : F - 1) - f;
+      constexpr int ws_behind = [] {
+        int n = 0;
+        for (int q = from; q <= f; ++q)
+          if (q % NT == 0 && q / NT < 3) n += 2;
+        return n;
+      }();
+      // the weights of product j went out with tile (j - 1) NT, behind that tile's piece
+      constexpr int w_at = (j - 1) * NT;
+      constexpr int w_behind = j == 0 ? D : [] {
+        int n = 0;
+        for (int q = w_at + 1; q <= f; ++q) {
+          if (q + D < F) ++n;
+          if (q % NT == 0 && q / NT < 3) n += 2;
+        }
+        return n;
+      }();
+      constexpr int behind = xs_behind + ws_behind;
+      twait<(i == 0 && w_behind < behind) ? w_behind : behind>();
+      ttie(x[f % (D + 1)]);
+      if constexpr (i == 0) {
+        ttie(w[j & 1][0]);
+        ttie(w[j & 1][1]);
+      }
+      if constexpr (f == 0) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          ttie(sw[m]);
+          sw[m] = (sw[m] & mask) | (0x7F7F7F7Fu & ~mask);
+        }
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          ttie(sx[q]);
+          sx[q] = (sx[q] & mask) | (0x7F7F7F7Fu & ~mask);
+        }
+      }
+      // the loads into the free stage, spread over the products (of two stages:
+      // the first half, the rest is their time to land)
+      constexpr int over = ST == 2 ? F / 2 : F, per = (WL + XL + over - 1) / over;
+      if constexpr (f < over)
+        static_for<per>([&](auto uc) {
+          request(next, b + ST - 1, out, std::integral_constant<int, per * f + decltype(uc)::value>{});
+        });
+#pragma unroll
+      for (int m = 0; m < 2; ++m) acc[m][i] = mfma_4_32<j>(w[j & 1][m], x[f % (D + 1)], acc[m][i], sw[m], sx[i]);
+    });
+  };
+  for (int b = 0;;) {
+    step(std::false_type{}, b);
+    place = place == (ST - 1) * SB ? 0 : place + SB;
+    if (++b >= count) break;
+    step(std::true_type{}, b);
+    place = place == (ST - 1) * SB ? 0 : place + SB;
+    if (++b >= count) break;
+  }
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  __syncthreads();  // LDS is free
+
+  // A wave's 32 rows of a tile and their columns go through its part of LDS, so
+  // that neighbouring lanes write neighbouring columns.
+  constexpr int CW = PAIR ? 32 : 64, LD = CW + 4;
+  float *const turn = reinterpret_cast<float *>(lds) + wave * 32 * 68;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int m = 0; m < (PAIR ? 1 : 2); ++m) {
+      f32x4_t v[4];  // columns 8 q + 4 h ..
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (PAIR) v[q][k] = situ_glu(acc[0][i][4 * q + k], acc[1][i][4 * q + k], g.beta, g.beta_lin);
+          else v[q][k] = acc[m][i][4 * q + k];
+        }
+      if (PAIR && g.out_kind == MX4_OUT_MX4) {
+        const int nb = n0 + 32 * wave;  // a block of the result
+        uint32_t top = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(v[q][k]) & 0x7FFFFFFFu);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+        const uint32_t sb = mx4_scale_byte(top, false);
+        const float inv = mx4_inverse(sb);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] *= inv;
+        // this half's codes, 16 bits of each 8 columns
+        uint32_t q01 = mx4_codes(__builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        uint32_t q23 = mx4_codes(__builtin_shufflevector(v[2], v[3], 0, 1, 2, 3, 4, 5, 6, 7));
+        if (sb == 255u) q01 = q23 = 0;
+        // the lower half writes columns 0..15 of the block, the upper one 16..31
+        const uint32_t mine = h ? q23 : q01, other = (uint32_t)__shfl_xor((int)(h ? q01 : q23), 32, 64);
+        const uint32_t lo = h ? other : mine, hi = h ? mine : other;  // columns 8 q + 0..3 and 8 q + 4..7
+        const u32x2_t o = {(lo & 0xFFFFu) | hi << 16, lo >> 16 | (hi & 0xFFFF0000u)};
+        const int r = 32 * i + r32;
+        if (r < c.n && nb < g.N) {
+          const long long p = c.row + r;
+          *reinterpret_cast<u32x2_t *>(static_cast<uint8_t *>(g.out) + p * g.ldo + nb / 2 + 8 * h) = o;
+          if (h == 0) g.os[p * g.ldos + nb / 32] = (uint8_t)sb;
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) *reinterpret_cast<f32x4_t *>(turn + r32 * LD + 32 * m + 8 * q + 4 * h) = v[q];
+      }
+    }
+    if (PAIR && g.out_kind == MX4_OUT_MX4) continue;
+    const int rows = min(32, c.n - 32 * i), n = n0 + CW * wave + 4 * (lane % (CW / 4));
+#pragma unroll 1
+    for (int r = lane / (CW / 4); r < rows; r += 256 / CW) {
+      f32x4_t v = *reinterpret_cast<const f32x4_t *>(turn + r * LD + 4 * (lane % (CW / 4)));
+      const long long p = c.row + 32 * i + r;
+      if (partial != nullptr) {
+        const int ldp = (g.N + 3) & ~3;
+        if (n < g.N) *reinterpret_cast<f32x4_t *>(partial + p * ldp + n) = v;
+        continue;
+      }
+      if (!PAIR && g.pair_weight != nullptr) v *= g.pair_weight[g.pair[p]];
+      if (g.out_kind == MX4_OUT_BF16) store4<MX4_OUT_BF16>(g, p, n, v);
+      else store4<MX4_OUT_F32>(g, p, n, v);
+    }
+  }
+}
+
+template <bool PAIR, bool SG>
+__global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4Args g, int splits, float *partial) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[TILE_LDS];
+  const int nb = (g.N + (PAIR ? 127 : 255)) / (PAIR ? 128 : 256), pairs = (g.K + 511) / 512;
+  const int chunks = g.chunks != nullptr ? *g.chunk_count : (g.P + TILE_ROWS - 1) / TILE_ROWS;
+  const int logical = xcd_logical(chunks * nb * splits);
+  if (logical < 0) return;
+  const int split = logical / (chunks * nb), item = logical - split * chunks * nb;
+  Chunk c;
+  int nblk;
+  if (g.chunks != nullptr) {
+    const int ci = item / nb;
+    nblk = item - ci * nb;
+    const int4 v = g.chunks[ci];
+    c = Chunk{v.x, v.y, v.z};
+  } else {
+    // a few column tiles next to each other, then the next rows: what an XCD works
+    // on at a time is near square
+    const int per = 4 * chunks, grp = item / per, in = item - grp * per, gn = min(4, nb - 4 * grp);
+    nblk = 4 * grp + in % gn;
+    const int ci = in / gn;
+    c = Chunk{0, TILE_ROWS * ci, min(TILE_ROWS, g.P - TILE_ROWS * ci)};
+  }
+  const int n0 = nblk * (PAIR ? 128 : 256);
+  const int stages = (g.K + 255) / 256;
+  const int first = 2 * (int)((long long)split * pairs / splits);
+  const int last = min(stages, 2 * (int)((long long)(split + 1) * pairs / splits));
+  float *part = splits > 1 ? partial + (long long)split * g.P * ((g.N + 3) & ~3) : nullptr;
+  switch ((c.n + 31) / 32) {
+    case 1: mx4_tile<1, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
+    case 2: mx4_tile<2, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
+    case 3: mx4_tile<3, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
+    case 4: mx4_tile<4, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
+    case 5:
+    case 6: mx4_tile<6, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
+    default: mx4_tile<8, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
+  }
+}
+
+// the splits' sums in order, four columns a thread
+template <int OUT>
+__global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args g, int splits, const float *partial) {
+  const int per = (g.N + 3) / 4;  // rows of partial are whole groups of four
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, stride = (long long)g.P * per;
+  if (i >= stride) return;
+  const int t = (int)(i / per), n = 4 * (int)(i - (long long)t * per);
+  const f32x4_t *p = reinterpret_cast<const f32x4_t *>(partial) + i;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) v += p[s * stride];
+  store4<OUT>(g, t, n, v);
+}
+
 template <int NT, int NW, int U>
 void stream_by_type(const Mx4Args &g, int max_items, hipStream_t st) {
   const dim3 gr((unsigned)std::min(max_items, 1 << 20)), blk(64 * NW);
@@ -408,32 +802,70 @@ hipError_t launch_dequantize4(const uint8_t *q, long long ldq, const uint8_t *qs
 }
 
 namespace {
-constexpr int CHUNK_ROWS = 64;
-int max_chunks(int E, int P) { return P / CHUNK_ROWS + std::min(E, P); }
+// scale rows that can be loaded 16 bytes at a time
+bool scales_in_groups(const Mx4Args &g) {
+  auto ok = [](const uint8_t *p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && ld % 4 == 0; };
+  return ok(g.sx, g.ldsx) && ok(g.sw[0], g.K / 32) && (g.w[1] == nullptr || ok(g.sw[1], g.K / 32));
+}
+void launch_tiles(const Mx4Args &g, long long items, int splits, float *partial, hipStream_t st) {
+  const dim3 gr((unsigned)((items * splits + 7) / 8 * 8)), blk(256);
+  if (scales_in_groups(g)) {
+    if (g.w[1] != nullptr) hipLaunchKernelGGL((mx4_tile_kernel<true, true>), gr, blk, 0, st, g, splits, partial);
+    else hipLaunchKernelGGL((mx4_tile_kernel<false, true>), gr, blk, 0, st, g, splits, partial);
+  } else {
+    if (g.w[1] != nullptr) hipLaunchKernelGGL((mx4_tile_kernel<true, false>), gr, blk, 0, st, g, splits, partial);
+    else hipLaunchKernelGGL((mx4_tile_kernel<false, false>), gr, blk, 0, st, g, splits, partial);
+  }
+}
+int max_chunks(int E, int P, int rows) { return P / rows + std::min(E, P); }
+// parts of K where the tiles are fewer than the CUs, of two stages at least
+int dense_splits(int T, int N, int K) {
+  const long long tiles = (long long)((T + 255) / 256) * ((N + 255) / 256), pairs = (K + 511) / 512;
+  return (int)std::max(1LL, std::min({256 / tiles, pairs, 16LL}));
+}
+bool dense_streams(int T) { return T <= 64; }
 }  // namespace
 
-size_t mx4_workspace_bytes(int, int, int) { return 0; }
+size_t mx4_workspace_bytes(int T, int N, int K) {
+  if (dense_streams(T)) return 0;
+  const int s = dense_splits(T, N, K);
+  return s > 1 ? (size_t)s * T * ((N + 3) / 4) * 16 : 0;
+}
 
-hipError_t launch_mx4_gemm(const Mx4Args &g, void *, hipStream_t st) {
+hipError_t launch_mx4_gemm(const Mx4Args &g, void *ws, hipStream_t st) {
   const int nb = (g.N + 31) / 32;
-  if (g.P <= 16) stream_by_type<1, 8, 4>(g, nb, st);
-  else stream_by_type<4, 4, 2>(g, (g.P + 63) / 64 * nb, st);
+  if (dense_streams(g.P)) {
+    if (g.P <= 16) stream_by_type<1, 8, 4>(g, nb, st);
+    else stream_by_type<4, 4, 2>(g, (g.P + 63) / 64 * nb, st);
+    return hipGetLastError();
+  }
+  const int splits = dense_splits(g.P, g.N, g.K);
+  launch_tiles(g, (long long)((g.P + 255) / 256) * ((g.N + 255) / 256), splits, static_cast<float *>(ws), st);
+  if (splits > 1) {
+    const dim3 jr((unsigned)(((long long)g.P * ((g.N + 3) / 4) + 255) / 256));
+    if (g.out_kind == MX4_OUT_BF16)
+      hipLaunchKernelGGL(mx4_join_kernel<MX4_OUT_BF16>, jr, dim3(256), 0, st, g, splits, static_cast<const float *>(ws));
+    else
+      hipLaunchKernelGGL(mx4_join_kernel<MX4_OUT_F32>, jr, dim3(256), 0, st, g, splits, static_cast<const float *>(ws));
+  }
   return hipGetLastError();
 }
 
-size_t mx4_expert_workspace_bytes(int E, int P, int, int) { return 256 + (size_t)max_chunks(E, P) * sizeof(int4); }
+size_t mx4_expert_workspace_bytes(int E, int P, int, int) { return 256 + (size_t)max_chunks(E, P, 64) * sizeof(int4); }
 
 hipError_t launch_mx4_expert(const Mx4Args &a, const int32_t *offsets, int E, void *ws, hipStream_t st) {
   Mx4Args g = a;
   int32_t *count = static_cast<int32_t *>(ws);
   int4 *chunks = reinterpret_cast<int4 *>(static_cast<char *>(ws) + 256);
-  const int cap = max_chunks(E, g.P);
-  hipLaunchKernelGGL(mx4_plan_kernel, dim3(1), dim3(1024), 0, st, offsets, E, g.P, CHUNK_ROWS, cap, chunks, count);
+  const bool stream = g.P < 8 * E;
+  const int rows = stream ? 64 : TILE_ROWS, cap = max_chunks(E, g.P, rows);
+  hipLaunchKernelGGL(mx4_plan_kernel, dim3(1), dim3(1024), 0, st, offsets, E, g.P, rows, cap, chunks, count);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   g.chunks = chunks;
   g.chunk_count = count;
-  stream_by_type<4, 4, 2>(g, cap * ((g.N + 31) / 32), st);
+  if (stream) stream_by_type<4, 4, 2>(g, cap * ((g.N + 31) / 32), st);
+  else launch_tiles(g, (long long)cap * ((g.N + (g.w[1] ? 127 : 255)) / (g.w[1] ? 128 : 256)), 1, nullptr, st);
   return hipGetLastError();
 }
 

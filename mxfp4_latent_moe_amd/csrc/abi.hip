@@ -662,8 +662,9 @@ static int mxfp4_expert_impl(const moe_mxfp4_expert_args *a, void *ws, size_t ws
   g.P = P;
   g.N = N;
   g.K = K;
-  return launch_mx4_expert(g, a->expert_offsets, a->n_experts, ws, static_cast<hipStream_t>(stream)) == hipSuccess
-             ? MOE_OK : MOE_EHIP;
+  g.offsets = a->expert_offsets;
+  g.n_experts = a->n_experts;
+  return launch_mx4_expert(g, ws, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
 // ---- the layer for a few tokens

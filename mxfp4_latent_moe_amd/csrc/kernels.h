@@ -251,7 +251,9 @@ struct Mx4Args {
   int out_kind, accumulate;
   int vec_out;            // rows of out are 16-byte (bf16: 8-byte) aligned
   int P, N, K;
-  const int4 *chunks;     // grouped: {expert, first row, rows, 0} and their number (NULL: dense)
+  const int32_t *offsets; // grouped: expert e's rows are offsets[e] .. offsets[e + 1] (NULL: dense)
+  int n_experts;
+  const int4 *chunks;     // set by the launch: {expert, first row, rows, 0} and their number
   const int32_t *chunk_count;
 };
 constexpr int MX4_MAX_E = 1024;  // experts of a grouped call
@@ -262,7 +264,7 @@ hipError_t launch_dequantize4(const uint8_t *q, long long ldq, const uint8_t *qs
 size_t mx4_workspace_bytes(int T, int N, int K);
 hipError_t launch_mx4_gemm(const Mx4Args &g, void *ws, hipStream_t st);
 size_t mx4_expert_workspace_bytes(int E, int P, int N, int K);
-hipError_t launch_mx4_expert(const Mx4Args &g, const int32_t *offsets, int E, void *ws, hipStream_t st);
+hipError_t launch_mx4_expert(const Mx4Args &g, void *ws, hipStream_t st);
 
 // ---- the layer for a few tokens
 constexpr int FEW_MAX_T = 4;

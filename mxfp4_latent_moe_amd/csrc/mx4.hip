@@ -139,13 +139,14 @@ __global__ __launch_bounds__(256) void dequantize4_kernel(const uint8_t *__restr
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-// c + 16 rows times 16 columns over 128 codes: a lane holds block lane / 16 of
-// row (column) lane % 16, and that block's scale byte
+// c + 16 rows times 16 columns over 128 codes, scaled by byte J of each operand's
+// scales: a lane holds one of four blocks of row (column) lane % 16
+template <int J>
 MOE_DEV f32x4_t mfma_4_16(u32x4_t w, u32x4_t x, f32x4_t c, uint32_t sw, uint32_t sx) {
   const i32x4_t w4 = __builtin_bit_cast(i32x4_t, w), x4 = __builtin_bit_cast(i32x4_t, x);
   const i32x8_t a = __builtin_shufflevector(w4, w4, 0, 1, 2, 3, -1, -1, -1, -1);
   const i32x8_t b = __builtin_shufflevector(x4, x4, 0, 1, 2, 3, -1, -1, -1, -1);
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, (int)sw, 0, (int)sx);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, J, (int)sw, J, (int)sx);
 }
 
 // an expert's rows [row, row + n) of a grouped product, or rows of the dense one
@@ -153,36 +154,48 @@ struct Chunk {
   int expert, row, n;
 };
 
-// Chunks of at most `rows` sorted rows, an expert's one after the other and, in
-// whole tiles of 32, of one size.  Bad offsets give wrong chunks but none outside
-// the P rows and the list's `cap`.
-__global__ __launch_bounds__(1024) void mx4_plan_kernel(const int32_t *offsets, int E, int P, int rows, int cap,
-                                                        int4 *chunks, int32_t *count) {
-  __shared__ int tot[16];
+// The experts' sorted rows as chunks, an expert's one after the other: experts of
+// up to `few` rows on the list few_list, one chunk each, the others on many_list in
+// chunks of at most `most` rows, in whole tiles of 64 of one size.  Bad offsets give
+// wrong chunks but none outside the P rows and the lists' sizes.
+__global__ __launch_bounds__(1024) void mx4_plan_kernel(const int32_t *offsets, int E, int P, int few, int most,
+                                                        int few_cap, int4 *few_list, int32_t *few_count, int many_cap,
+                                                        int4 *many_list, int32_t *many_count) {
+  __shared__ int tot[2][16];
   const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
   int lo = 0, ne = 0;
   if (e < E) {
     lo = min(max(offsets[e], 0), P);
     ne = min(max(offsets[e + 1], lo), P) - lo;
   }
-  const int nch = (ne + rows - 1) / rows;
-  int x = nch;
+  int n[2] = {ne > 0 && ne <= few ? 1 : 0, ne > few ? (ne + most - 1) / most : 0}, at[2], sum[2] = {0, 0};
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
+  for (int l = 0; l < 2; ++l) {
+    int x = n[l];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(x, d, 64);
+      if (lane >= d) x += y;
+    }
+    if (lane == 63) tot[l][wave] = x;
+    at[l] = x - n[l];
   }
-  if (lane == 63) tot[wave] = x;
   __syncthreads();
-  int at = x - nch, sum = 0;
-  for (int w = 0; w < 16; ++w) {
-    if (w < wave) at += tot[w];
-    sum += tot[w];
+  for (int w = 0; w < 16; ++w)
+#pragma unroll
+    for (int l = 0; l < 2; ++l) {
+      if (w < wave) at[l] += tot[l][w];
+      sum[l] += tot[l][w];
+    }
+  if (n[0] && at[0] < few_cap) few_list[at[0]] = int4{e, lo, ne, 0};
+  const int each = n[1] > 0 ? ((ne + n[1] - 1) / n[1] + 63) / 64 * 64 : 0;
+  for (int i = 0; i < n[1] && at[1] + i < many_cap; ++i)
+    if (i * each < ne) many_list[at[1] + i] = int4{e, lo + i * each, min(each, ne - i * each), 0};
+    else many_list[at[1] + i] = int4{e, lo, 0, 0};
+  if (e == 0) {
+    *few_count = min(sum[0], few_cap);
+    *many_count = min(sum[1], many_cap);
   }
-  const int each = nch > 0 ? ((ne + nch - 1) / nch + 31) / 32 * 32 : 0;
-  for (int i = 0; i < nch && at + i < cap; ++i)
-    chunks[at + i] = int4{e, lo + i * each, min(each, ne - i * each), 0};
-  if (e == 0) *count = min(sum, cap);
 }
 
 // four columns n .. of row p in the output's type
@@ -216,160 +229,6 @@ MOE_DEV void store4(const Mx4Args &g, long long p, int n, f32x4_t v) {
 // the row of x that sorted row p of the product reads
 MOE_DEV int x_row(const Mx4Args &g, int p) { return g.map == nullptr ? p : g.map[p] / g.div; }
 
-// Few rows: the weights are the whole cost.  A work-group owns 32 columns of the
-// result (of a pair, 32 weight rows of each matrix) and 16 NT rows; its NW waves
-// take steps of 128 inputs in turn, so that at any time they read a contiguous
-// NW * 64 bytes of each weight row, U steps in flight each.  Both operands come
-// straight from memory, the rows from the L2.  The waves' sums meet in LDS and
-// are added in wave order.
-template <int NT, int NW, int U, bool PAIR, int OUT>
-__global__ __launch_bounds__(64 * NW) void mx4_stream_kernel(Mx4Args g) {
-  constexpr int NM = PAIR ? 2 : 1;
-  __shared__ f32x4_t part[NW][NM][2][NT][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, kg = lane >> 4;
-  const int K = g.K, kbytes = K / 2, kb = K / 32, steps = (K + 127) / 128;
-  const int nb = (g.N + 31) / 32;
-  const int total = (g.chunks != nullptr ? *g.chunk_count : (g.P + 16 * NT - 1) / (16 * NT)) * nb;
-  for (int item = blockIdx.x; item < total; item += gridDim.x) {
-    const int ci = item / nb, n0 = 32 * (item - ci * nb);
-    Chunk c{0, 16 * NT * ci, min(16 * NT, g.P - 16 * NT * ci)};
-    if (g.chunks != nullptr) {
-      const int4 v = g.chunks[ci];
-      c = Chunk{v.x, v.y, v.z};
-    }
-    const int nrows = min(32, g.N - n0);
-    __amdgpu_buffer_rsrc_t wr[NM], sr[NM];
-#pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      const long long row = (long long)c.expert * g.N + n0;
-      wr[m] = make_rsrc(g.w[m] + row * kbytes, (uint32_t)nrows * (uint32_t)kbytes);
-      sr[m] = make_rsrc(g.sw[m] + row * kb, (uint32_t)nrows * (uint32_t)kb);
-    }
-    // gathered rows are found from the first row of x, others from the chunk's own
-    const long long base = g.map != nullptr ? 0 : c.row;
-    const int xrows = g.map != nullptr ? g.x_rows : c.n;
-    const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + base * g.ldx, (uint32_t)((xrows - 1) * g.ldx + kbytes));
-    const __amdgpu_buffer_rsrc_t xsr = make_rsrc(g.sx + base * g.ldsx, (uint32_t)((xrows - 1) * g.ldsx + kb));
-    uint32_t wo[2], so[2], xo[NT], xso[NT];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int r = min(16 * m + r16, nrows - 1);
-      wo[m] = (uint32_t)r * (uint32_t)kbytes + 16 * kg;
-      so[m] = (uint32_t)r * (uint32_t)kb + kg;
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int r = x_row(g, c.row + min(16 * i + r16, c.n - 1)) - (int)base;
-      xo[i] = (uint32_t)r * (uint32_t)g.ldx + 16 * kg;
-      xso[i] = (uint32_t)r * (uint32_t)g.ldsx + kg;
-    }
-    f32x4_t acc[NM][2][NT];
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) acc[m][j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int b0 = wave; b0 < steps; b0 += NW * U) {
-      u32x4_t w[U][NM][2], x[U][NT];
-      uint32_t sw[U][NM][2], sx[U][NT];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // steps past the end, and lanes whose block is past it, read out of range: codes of zero
-        const int b = b0 + NW * u;
-        const bool in = 4 * b + kg < kb;
-        const uint32_t past = in ? 0u : 0x80000000u;
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            w[u][m][j] = buf_load16(wr[m], wo[j] + past, 64u * b);
-            sw[u][m][j] = __builtin_amdgcn_raw_buffer_load_b8(sr[m], so[j] + past, 4u * b, 0);
-          }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          x[u][i] = buf_load16(xr, xo[i] + past, 64u * b);
-          sx[u][i] = __builtin_amdgcn_raw_buffer_load_b8(xsr, xso[i] + past, 4u * b, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);  // every load of the round is on its way before the first product
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-              acc[m][j][i] = mfma_4_16(w[u][m][j], x[u][i], acc[m][j][i], sw[u][m][j], sx[u][i]);
-    }
-#pragma unroll
-    for (int m = 0; m < NM; ++m)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < NT; ++i) part[wave][m][j][i][lane] = acc[m][j][i];
-    __syncthreads();
-    // eight neighbouring threads a row, four columns each
-    for (int e = threadIdx.x; e < 128 * NT; e += 64 * NW) {
-      const int t = e >> 3, j = e >> 2 & 1, h = e & 3, l = 16 * h + (t & 15), i = t >> 4;
-      f32x4_t v[NM];
-#pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        v[m] = part[0][m][j][i][l];
-#pragma unroll
-        for (int q = 1; q < NW; ++q) v[m] += part[q][m][j][i][l];
-      }
-      if constexpr (PAIR) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[0][r] = situ_glu(v[0][r], v[1][r], g.beta, g.beta_lin);
-      }
-      const int n = n0 + 16 * j + 4 * h;
-      const long long p = c.row + t;
-      if (!PAIR && g.pair_weight != nullptr && t < c.n) v[0] *= g.pair_weight[g.pair[p]];
-      if constexpr (OUT == MX4_OUT_MX4) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) m = max(m, __float_as_uint(v[0][r]) & 0x7FFFFFFFu);
-        m = max4(m);
-        m = max(m, (uint32_t)__shfl_xor((int)m, 4, 64));
-        const uint32_t sb = mx4_scale_byte(m, false);
-        v[0] *= mx4_inverse(sb);
-        uint32_t q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0][0], v[0][1], 1.0f, 0);
-        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0][2], v[0][3], 1.0f, 1);
-        if (t < c.n) {
-          *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(g.out) + p * g.ldo + n / 2) =
-              sb == 255u ? (uint16_t)0 : (uint16_t)q;
-          if ((e & 7) == 0) g.os[p * g.ldos + n / 32] = (uint8_t)sb;
-        }
-      } else {
-        if (t < c.n) store4<OUT>(g, p, n, v[0]);
-      }
-    }
-    __syncthreads();  // part is free again
-  }
-}
-
-// ---- many rows
-// A work-group of four waves, one a SIMD, owns 256 weight rows (of a pair, 128 of
-// each matrix) and up to 256 rows of x; a wave of it 64 weight rows and all of
-// the rows, 2 x NT tiles of 32 x 32.  Both operands pass through ST LDS stages of
-// 256 inputs, filled by direct loads of rows' whole 128 bytes between the products.
-//
-// A row's 128 bytes are eight pieces of 16, a block of 32 codes each; piece p of
-// row r lies at position p ^ (r / 2 % 8), so the 16 rows that a quarter wave reads
-// at once, two to a 256-byte line of LDS, fall on different banks.  Product j of a
-// stage takes piece 4 h + j from the lanes of half h: the two halves of the
-// instruction's K need not be neighbours in memory, and the four scale bytes that
-// a lane needs in a stage are then one dword, from which the instruction selects
-// byte j.  Scales come into LDS 16 bytes a row, two stages at a time.
-//
-// SG: scale rows are whole dwords apart and aligned, so that those 16 bytes can be
-// loaded directly; else they come byte by byte through registers.
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
-
 // 16 bytes of LDS at a + O, issued without waiting
 template <int O>
 MOE_DEV void tread(uint32_t a, u32x4_t &v) {
@@ -391,6 +250,370 @@ MOE_DEV void ttie(V &v) {
   asm volatile("" : "+v"(v));
 }
 
+// The chunk of number `want` where no list of them was made: every work-group
+// counts the experts' chunks itself.  NW waves; false: there are fewer.
+template <int NW>
+MOE_DEV bool find_chunk(const Mx4Args &g, int rows, int want, Chunk &c, int *lds) {
+  constexpr int PER = MX4_MAX_E / (64 * NW);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int lo[PER], ne[PER], n = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = PER * tid + i;
+    lo[i] = ne[i] = 0;
+    if (e < g.n_experts) {
+      lo[i] = min(max(g.offsets[e], 0), g.P);
+      ne[i] = min(max(g.offsets[e + 1], lo[i]), g.P) - lo[i];
+      n += (ne[i] + rows - 1) / rows;
+    }
+  }
+  int x = n;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  if (lane == 63) lds[wave] = x;
+  if (tid == 0) lds[NW + 2] = 0;
+  __syncthreads();
+  int at = x - n;
+#pragma unroll
+  for (int w = 0; w < NW; ++w)
+    if (w < wave) at += lds[w];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int k = want - at, nch = (ne[i] + rows - 1) / rows;
+    if (k >= 0 && k < nch) {
+      lds[NW] = PER * tid + i;
+      lds[NW + 1] = lo[i] + k * rows;
+      lds[NW + 2] = min(rows, ne[i] - k * rows);
+    }
+    at += nch;
+  }
+  __syncthreads();
+  c = Chunk{lds[NW], lds[NW + 1], lds[NW + 2]};
+  return c.n > 0;
+}
+
+// ---- few rows: the weights are the whole cost
+//
+// A wave owns 32 weight rows (32 columns of the result, of a pair 16 of each
+// matrix) and 16 NT rows of x, and has a ring of its own in LDS, ST stages of 256
+// inputs, that direct loads of rows' whole 128 bytes fill: no wave waits for
+// another while it streams, and the waves of a CU keep some 100 KB on their way.
+// x and the scales come straight to registers, a stage ahead (the rows stay in the
+// L2).  KS waves of a work-group of NW share their columns and take parts of K;
+// their sums meet in LDS and are added in order.
+//
+// In LDS piece p (16 bytes, a block) of row r lies at position p ^ (r / 2 % 8), as
+// the 16 rows that a quarter wave reads at once, two to a 256-byte line, then fall
+// on different banks.  Product j of a stage takes piece 2 kg + j from the lanes of
+// group kg (the groups' K need not be neighbours in memory), so that a lane's two
+// scale bytes of a stage are neighbours, of which the instruction selects one.
+// EVEN: scale rows are even distances apart, so that the two load as one.
+constexpr int STREAM_ST = 4, STREAM_STAGE = 32 * 128;
+
+// 16 bytes a lane straight into LDS (the host's pass over this code knows of 4 only)
+MOE_DEV void lds_load(__amdgpu_buffer_rsrc_t r, uint8_t *to, uint32_t voff, uint32_t soff) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, voff, soff, 0, 0);
+#endif
+}
+
+// two neighbouring scale bytes
+template <bool EVEN>
+MOE_DEV uint32_t load_scales(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t at) {
+  if constexpr (EVEN) {
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, at, 0);
+  } else {
+    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b8(r, off, at, 0);
+    return lo | (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(r, off + 1, at, 0) << 8;
+  }
+}
+
+// what a stage takes from registers: pieces of x, scales of x and of the weights
+template <int NT>
+struct StreamRegs {
+  u32x4_t x[NT][2];
+  uint32_t sx[NT], sw[2];
+};
+
+template <int NT, bool PAIR, bool EVEN, int KS>
+MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *lds) {
+  constexpr int ST = STREAM_ST, SB = STREAM_STAGE, DL = 4;
+  constexpr int RL = NT * (EVEN ? 3 : 4) + 2 * (EVEN ? 1 : 2);  // register loads of a stage
+  constexpr int CW = PAIR ? 16 : 32;
+  const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kg = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kbytes = g.K / 2, kb = g.K / 32, stages = (g.K + 255) / 256;
+  const int n0 = CW * block, part = KS == 1 ? 0 : wave % KS;
+  // a wave whose columns are past the last one only keeps the barriers whole
+  const int nrows = __builtin_amdgcn_readfirstlane(max(min(CW, g.N - n0), 0));
+  const int first = (int)((long long)part * stages / KS);
+  const int count = nrows > 0 ? (int)((long long)(part + 1) * stages / KS) - first : 0;
+  uint8_t *const ring = lds + wave * (ST * SB);
+  constexpr uint32_t OUT = 0x80000000u;  // past the end of every buffer
+
+  __amdgpu_buffer_rsrc_t wr[PAIR ? 2 : 1], sr[PAIR ? 2 : 1];
+#pragma unroll
+  for (int m = 0; m < (PAIR ? 2 : 1); ++m) {
+    const long long row = (long long)c.expert * g.N + n0;
+    wr[m] = make_rsrc(g.w[m] + row * kbytes, (uint32_t)nrows * (uint32_t)kbytes);
+    sr[m] = make_rsrc(g.sw[m] + row * kb, (uint32_t)nrows * (uint32_t)kb);
+  }
+  // gathered rows are found from the first row of x, others from the chunk's own
+  const long long base = g.map != nullptr ? 0 : c.row;
+  const int xrows = g.map != nullptr ? g.x_rows : c.n;
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + base * g.ldx, (uint32_t)((xrows - 1) * g.ldx + kbytes));
+  const __amdgpu_buffer_rsrc_t xsr = make_rsrc(g.sx + base * g.ldsx, (uint32_t)((xrows - 1) * g.ldsx + kb));
+  const int l8 = lane >> 3;
+  uint32_t piece[2], vw[DL], so[2], xo[NT], xso[NT];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) piece[q] = 16 * ((lane & 7) ^ (4 * q + (lane >> 4)));
+#pragma unroll
+  for (int u = 0; u < DL; ++u)  // 8 rows a load; the second matrix's are loads 2 and 3
+    vw[u] = (uint32_t)(8 * (PAIR ? u & 1 : u) + l8) * (uint32_t)kbytes + piece[u & 1];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) so[m] = (uint32_t)min((PAIR ? 0 : 16 * m) + r16, nrows - 1) * (uint32_t)kb + 2 * kg;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    // rows past the chunk read out of range
+    const bool in = 16 * i + r16 < c.n;
+    const uint32_t r = in ? (uint32_t)(x_row(g, c.row + 16 * i + r16) - (int)base) : 0u;
+    xo[i] = in ? r * (uint32_t)g.ldx + 32 * kg : OUT;
+    xso[i] = in ? r * (uint32_t)g.ldsx + 2 * kg : OUT;
+  }
+
+  auto request = [&](int s) {  // stage s of this wave's part
+    uint8_t *const at = ring + (s % ST) * SB;
+    const uint32_t k0 = 128u * (first + s);
+    // of a stage that ends inside, pieces past K read out of range: zeros
+    const uint32_t past[2] = {k0 + piece[0] < (uint32_t)kbytes ? 0u : OUT, k0 + piece[1] < (uint32_t)kbytes ? 0u : OUT};
+#pragma unroll
+    for (int u = 0; u < DL; ++u)
+      lds_load(wr[PAIR ? u >> 1 : 0], at + 1024 * u, vw[u] | past[u & 1], k0);
+  };
+  using Regs = StreamRegs<NT>;
+  auto load = [&](Regs &v, int s) {
+    const uint32_t k0 = 128u * (first + s), b0 = 8u * (first + s);
+    const uint32_t past = b0 + 2 * kg < (uint32_t)kb ? 0u : OUT, past2 = b0 + 2 * kg + 1 < (uint32_t)kb ? 0u : OUT;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      v.x[i][0] = buf_load16(xr, xo[i] | past, k0);
+      v.x[i][1] = buf_load16(xr, (xo[i] + 16) | past2, k0);
+      v.sx[i] = load_scales<EVEN>(xsr, xso[i] | past, b0);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) v.sw[m] = load_scales<EVEN>(sr[PAIR ? m : 0], so[m] | past, b0);
+  };
+
+  f32x4_t acc[2][NT];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint32_t frag[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) frag[j] = lds_addr(ring) + 128 * r16 + 16 * ((2 * kg + j) ^ (r16 >> 1));
+  auto step = [&](auto morec, int s, Regs &now, Regs &next) {
+    constexpr bool more = decltype(morec)::value;  // a stage is left to request
+    load(next, min(s + 1, count - 1));
+    __builtin_amdgcn_sched_barrier(0);  // the waits count loads in this order
+    if constexpr (more) request(s + ST - 1);
+    // this stage and its registers have landed; requested since are the next two
+    // stages and the next registers (near the end at most the registers)
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm((more ? DL * (ST - 2) : 0) + RL));
+    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t at = (s % ST) * SB;
+    u32x4_t w[2][2];
+    tread<0>(frag[0] + at, w[0][0]);
+    tread<2048>(frag[0] + at, w[1][0]);
+    tread<0>(frag[1] + at, w[0][1]);
+    tread<2048>(frag[1] + at, w[1][1]);
+    // scale bytes past K are of other rows: one in their place
+    const int in = kb - 8 * (first + s) - 2 * kg;
+    const uint32_t mask = in >= 2 ? 0xFFFFu : in <= 0 ? 0u : 0xFFu;
+    uint32_t sw[2], sx[NT];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) sw[m] = (now.sw[m] & mask) | (0x7F7Fu & ~mask);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sx[i] = (now.sx[i] & mask) | (0x7F7Fu & ~mask);
+    twait<2>();
+    ttie(w[0][0]);
+    ttie(w[1][0]);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[m][i] = mfma_4_16<0>(w[m][0], now.x[i][0], acc[m][i], sw[m], sx[i]);
+    twait<0>();
+    ttie(w[0][1]);
+    ttie(w[1][1]);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[m][i] = mfma_4_16<1>(w[m][1], now.x[i][1], acc[m][i], sw[m], sx[i]);
+  };
+  if (count > 0) {
+    Regs a, b;
+    load(a, 0);
+    for (int s = 0; s < min(ST - 1, count); ++s) request(s);
+    auto turn = [&] {  // the next registers become these
+#pragma unroll
+      for (int m = 0; m < 2; ++m) a.sw[m] = b.sw[m];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        a.sx[i] = b.sx[i];
+        a.x[i][0] = b.x[i][0];
+        a.x[i][1] = b.x[i][1];
+      }
+    };
+    const std::integral_constant<bool, true> more;
+    const std::integral_constant<bool, false> none;
+    const int most = count - (ST - 1);
+    int s = 0;
+    for (; s + 1 < most; s += 2) {
+      step(more, s, a, b);
+      step(more, s + 1, b, a);
+    }
+    if (s < most) {
+      step(more, s++, a, b);
+      turn();
+    }
+    for (; s < count; ++s) {
+      step(none, s, a, b);
+      turn();
+    }
+  }
+
+  if constexpr (KS > 1) {
+    f32x4_t *const mine = reinterpret_cast<f32x4_t *>(ring);  // its own loads have landed
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) mine[64 * (NT * m + i) + lane] = acc[m][i];
+    __syncthreads();
+    // tile by tile in turn over the waves that share them
+    const int w0 = wave - part;
+    for (int t = part; t < 2 * NT; t += KS) {
+      f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+      for (int q = 0; q < KS; ++q)
+        v += reinterpret_cast<const f32x4_t *>(lds + (w0 + q) * (ST * SB))[64 * t + lane];
+      const int m = t / NT, r = 16 * (t % NT) + r16, n = n0 + 16 * m + 4 * kg;
+      if (r < c.n) {
+        if (g.out_kind == MX4_OUT_BF16) store4<MX4_OUT_BF16>(g, c.row + r, n, v);
+        else store4<MX4_OUT_F32>(g, c.row + r, n, v);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int r = 16 * i + r16;
+    const long long p = c.row + r;
+    if constexpr (PAIR) {
+      f32x4_t v;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = situ_glu(acc[0][i][k], acc[1][i][k], g.beta, g.beta_lin);
+      const int n = n0 + 4 * kg;
+      if (g.out_kind == MX4_OUT_MX4) {
+        // a block of the result is this wave's columns and its neighbour's
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+        top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+        uint32_t *const tops = reinterpret_cast<uint32_t *>(lds);
+        __syncthreads();  // rings (and the tops of the tile before) are done with
+        if (kg == 0) tops[16 * wave + r16] = top;
+        __syncthreads();
+        top = max(top, tops[16 * (wave ^ 1) + r16]);
+        const uint32_t sb = mx4_scale_byte(top, false);
+        v *= mx4_inverse(sb);
+        uint32_t q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], 1.0f, 0);
+        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], 1.0f, 1);
+        if (r < c.n && n < g.N) {
+          *reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(g.out) + p * g.ldo + n / 2) =
+              sb == 255u ? (uint16_t)0 : (uint16_t)q;
+          if (lane < 16 && n0 % 32 == 0) g.os[p * g.ldos + n0 / 32] = (uint8_t)sb;
+        }
+      } else if (r < c.n) {
+        if (g.out_kind == MX4_OUT_BF16) store4<MX4_OUT_BF16>(g, p, n, v);
+        else store4<MX4_OUT_F32>(g, p, n, v);
+      }
+    } else if (r < c.n) {
+      const float pw = g.pair_weight != nullptr ? g.pair_weight[g.pair[p]] : 1.f;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const f32x4_t v = acc[m][i] * pw;
+        if (g.out_kind == MX4_OUT_BF16) store4<MX4_OUT_BF16>(g, p, n0 + 16 * m + 4 * kg, v);
+        else store4<MX4_OUT_F32>(g, p, n0 + 16 * m + 4 * kg, v);
+      }
+    }
+  }
+}
+
+template <int MAXT, bool PAIR, bool EVEN, int KS>
+MOE_DEV void mx4_stream_rows(const Mx4Args &g, const Chunk &c, int block, uint8_t *lds) {
+  if (MAXT == 1 || c.n <= 16) mx4_stream<1, PAIR, EVEN, KS>(g, c, block, lds);
+  else if (MAXT == 2 || c.n <= 32) mx4_stream<(MAXT < 2 ? MAXT : 2), PAIR, EVEN, KS>(g, c, block, lds);
+  else mx4_stream<MAXT, PAIR, EVEN, KS>(g, c, block, lds);
+}
+
+// work-groups of 4 waves with a block of columns each, two on a CU (grouped), or of
+// 8 that share one (dense); chunks of at most 16 MAXT rows
+template <int MAXT, bool PAIR, bool EVEN, int KS>
+__global__ __launch_bounds__(KS == 1 ? 256 : 512, 2) void mx4_stream_kernel(Mx4Args g) {
+  constexpr int NW = KS == 1 ? 4 : 8, BLOCKS = NW / KS;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * STREAM_ST * STREAM_STAGE];
+  const int nb = ((g.N + (PAIR ? 15 : 31)) / (PAIR ? 16 : 32) + BLOCKS - 1) / BLOCKS;  // work-groups a chunk
+  Chunk c;
+  int nblk;
+  if (KS > 1) {  // dense
+    const int logical = xcd_logical((g.P + 16 * MAXT - 1) / (16 * MAXT) * nb);
+    if (logical < 0) return;
+    const int ci = logical / nb;
+    nblk = logical - ci * nb;
+    c = Chunk{0, 16 * MAXT * ci, min(16 * MAXT, g.P - 16 * MAXT * ci)};
+  } else if (g.chunks != nullptr) {
+    const int logical = xcd_logical(*g.chunk_count * nb);
+    if (logical < 0) return;
+    const int ci = logical / nb;
+    nblk = logical - ci * nb;
+    const int4 v = g.chunks[ci];
+    c = Chunk{v.x, v.y, v.z};
+  } else {
+    const int ci = blockIdx.x / nb;
+    nblk = blockIdx.x - ci * nb;
+    if (!find_chunk<NW>(g, 16 * MAXT, ci, c, reinterpret_cast<int *>(lds))) return;
+    __syncthreads();  // lds is the rings' from here on
+  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int block = nblk * BLOCKS + wave / KS;
+  // the same in every lane, which buffer descriptors need
+  c = Chunk{__builtin_amdgcn_readfirstlane(c.expert), __builtin_amdgcn_readfirstlane(c.row),
+            __builtin_amdgcn_readfirstlane(c.n)};
+  mx4_stream_rows<MAXT, PAIR, EVEN, KS>(g, c, block, lds);
+}
+
+// ---- many rows
+// A work-group of eight waves owns 256 weight rows (of a pair, 128 of each matrix)
+// and 64 NT rows of x; a wave of it 64 weight rows and half of the rows, 2 x NT
+// tiles of 32 x 32.  Both operands pass through ST LDS stages of
+// 256 inputs, filled by direct loads of rows' whole 128 bytes between the products.
+//
+// A row's 128 bytes are eight pieces of 16, a block of 32 codes each; piece p of
+// row r lies at position p ^ (r / 2 % 8), so the 16 rows that a quarter wave reads
+// at once, two to a 256-byte line of LDS, fall on different banks.  Product j of a
+// stage takes piece 4 h + j from the lanes of half h: the two halves of the
+// instruction's K need not be neighbours in memory, and the four scale bytes that
+// a lane needs in a stage are then one dword, from which the instruction selects
+// byte j.  Scales come into LDS 16 bytes a row, two stages at a time.
+//
+// SG: scale rows are whole dwords apart and aligned, so that those 16 bytes can be
+// loaded directly; else they come byte by byte through registers.
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
 // c + 32 rows times 32 columns over 64 codes, scaled by byte J of each operand's scales
 template <int J>
 MOE_DEV f32x16_t mfma_4_32(u32x4_t w, u32x4_t x, f32x16_t c, uint32_t sw, uint32_t sx) {
@@ -402,21 +625,21 @@ MOE_DEV f32x16_t mfma_4_32(u32x4_t w, u32x4_t x, f32x16_t c, uint32_t sw, uint32
 
 constexpr int TILE_ROWS = 256;    // rows of x
 constexpr int TILE_COLS = 256;    // weight rows
-constexpr int stages_of(int nt) { return nt == 1 ? 4 : nt <= 4 ? 3 : 2; }
-constexpr int stage_bytes(int nt) { return (TILE_COLS + 32 * nt) * 128; }
 constexpr int GROUP_BYTES = (TILE_COLS + TILE_ROWS) * 16;  // scales of two stages
+constexpr int stages_of(int nt) { return nt <= 2 ? 3 : 2; }
+constexpr int stage_bytes(int nt) { return (TILE_COLS + 64 * nt) * 128; }
 constexpr int tile_lds(int nt) { return stages_of(nt) * stage_bytes(nt) + 2 * GROUP_BYTES; }
 constexpr int max_lds(int nt) { return nt == 0 ? 0 : tile_lds(nt) > max_lds(nt - 1) ? tile_lds(nt) : max_lds(nt - 1); }
-constexpr int TILE_LDS = max_lds(8);
+constexpr int TILE_LDS = max_lds(4);
 static_assert(TILE_LDS <= 160 * 1024, "LDS of a CU");
 
 // rows c of x times weight rows of columns n0 .., stages first .. first + count - 1 of K (first even)
 template <int NT, bool PAIR, bool SG>
 MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int count, float *partial, uint8_t *lds) {
   constexpr int ST = stages_of(NT), SB = stage_bytes(NT), GB = GROUP_BYTES;
-  constexpr int WL = 8, XL = NT;  // direct loads of a wave per stage, 8 rows each
+  constexpr int WL = 4, XL = NT;  // direct loads of a wave per stage, 8 rows each
   const int tid = threadIdx.x, lane = tid & 63, r32 = lane & 31, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 3, wt = wave >> 2;
   const int kbytes = g.K / 2, kb = g.K / 32;
   const int ncols = min(PAIR ? TILE_COLS / 2 : TILE_COLS, g.N - n0);
   uint8_t *const groups = lds + ST * SB;
@@ -444,58 +667,49 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
   for (int q = 0; q < 2; ++q) piece[q] = 16 * ((lane & 7) ^ (4 * q + (lane >> 4)));
 #pragma unroll
   for (int u = 0; u < WL; ++u) {
-    const int n = PAIR ? 32 * wave + 8 * (u & 3) + l8 : 64 * wave + 8 * u + l8;
+    const int n = 32 * (PAIR ? wave >> 1 : wave) + 8 * u + l8;  // of a pair, even waves the first matrix's rows
     vw[u] = (uint32_t)n * (uint32_t)kbytes + piece[u & 1];
   }
 #pragma unroll
   for (int u = 0; u < XL; ++u) {
-    const int r = 8 * (4 * u + wave) + l8;
+    const int r = 8 * (8 * u + wave) + l8;
     vx[u] = r < c.n ? row_of(r) * (uint32_t)g.ldx + piece[wave & 1] : OUT;
   }
-  auto past = [&](int b, uint32_t p) {  // of a stage that ends inside, or after the last
-    return b < count && 128u * (first + b) + p < (uint32_t)kbytes ? 0u : OUT;
-  };
+  // what to add where stage b ends inside; stages after the last are read as the last, unused
+  auto past = [&](int b, uint32_t p) { return 128u * (first + min(b, count - 1)) + p < (uint32_t)kbytes ? 0u : OUT; };
   // load u of stage b, to the place at `place` of the ring
   auto request = [&](uint32_t place, int b, const uint32_t (&out)[2], auto uc) {
     constexpr int u = decltype(uc)::value;
     uint8_t *const at = lds + place;
-    const uint32_t k0 = 128u * (first + b);
+    const uint32_t k0 = 128u * (first + min(b, count - 1));
     if constexpr (u < WL)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[PAIR && u >= 4 ? 1 : 0], (lds_void *)(at + (64 * wave + 8 * u) * 128), 16,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr[PAIR ? wave & 1 : 0], (lds_void *)(at + (32 * wave + 8 * u) * 128), 16,
                                                vw[u] | out[u & 1], k0, 0, 0);
     else if constexpr (u < WL + XL)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          xr, (lds_void *)(at + (TILE_COLS + 8 * (4 * (u - WL) + wave)) * 128), 16, vx[u - WL] | out[wave & 1], k0, 0, 0);
+          xr, (lds_void *)(at + (TILE_COLS + 8 * (8 * (u - WL) + wave)) * 128), 16, vx[u - WL] | out[wave & 1], k0, 0, 0);
   };
-  // scales of stages 2 q and 2 q + 1: [row][16]; of a pair first one matrix's 128 rows, then the other's
-  const int sn = PAIR ? 64 * (wave & 1) + lane : 64 * wave + lane, st = 64 * wave + lane;
-  const uint32_t vs = (uint32_t)sn * (uint32_t)kb;
-  const uint32_t vt = st < c.n ? row_of(st) * (uint32_t)g.ldsx : OUT;
-  u32x4_t held[2];  // without SG: on their way through registers
+  // scales of stages 2 q and 2 q + 1: [row][16], a row a lane; waves 0 to 3 the
+  // weights' (of a pair first one matrix's 128 rows, then the other's), the others x's
+  const int sr_row = 64 * (PAIR && wt == 0 ? wn & 1 : wn) + lane;
+  const uint32_t vs = wt == 0 ? (uint32_t)sr_row * (uint32_t)kb : sr_row < c.n ? row_of(sr_row) * (uint32_t)g.ldsx : OUT;
+  const __amdgpu_buffer_rsrc_t srsrc = wt != 0 ? xsr : PAIR && wn >= 2 ? sr[PAIR ? 1 : 0] : sr[0];
+  u32x4_t held;  // without SG: on their way through registers
   auto request_scales = [&](int q) {
-    const uint32_t at = 16u * (first / 2 + q);
+    const uint32_t at = 16u * (first / 2 + min(q, (count - 1) / 2));
     if constexpr (SG) {
-      uint8_t *const to = groups + (q & 1) * GB;
-      const uint32_t none = 2 * q < count ? 0u : OUT;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sr[PAIR ? wave >> 1 : 0], (lds_void *)(to + 1024 * wave), 16, vs | none, at, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xsr, (lds_void *)(to + TILE_COLS * 16 + 1024 * wave), 16, vt | none, at, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(srsrc, (lds_void *)(groups + (q & 1) * GB + 1024 * wave), 16,
+                                               vs, at, 0, 0);
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const uint32_t none = at + i < (uint32_t)kb ? 0u : OUT;
-        const uint32_t a = __builtin_amdgcn_raw_buffer_load_b8(sr[PAIR ? wave >> 1 : 0], vs | none, at + i, 0);
-        const uint32_t b = __builtin_amdgcn_raw_buffer_load_b8(xsr, vt | none, at + i, 0);
-        held[0][i >> 2] = i & 3 ? held[0][i >> 2] | a << (8 * (i & 3)) : a;
-        held[1][i >> 2] = i & 3 ? held[1][i >> 2] | b << (8 * (i & 3)) : b;
+        const uint32_t a = __builtin_amdgcn_raw_buffer_load_b8(srsrc, vs | (at + i < (uint32_t)kb ? 0u : OUT), at + i, 0);
+        held[i >> 2] = i & 3 ? held[i >> 2] | a << (8 * (i & 3)) : a;
       }
     }
   };
   auto put_scales = [&](int q) {
-    if constexpr (!SG) {
-      u32x4_t *const to = reinterpret_cast<u32x4_t *>(groups + (q & 1) * GB);
-      to[tid] = held[0];
-      to[TILE_COLS + tid] = held[1];
-    }
+    if constexpr (!SG) reinterpret_cast<u32x4_t *>(groups + (q & 1) * GB)[tid] = held;
   };
 
   f32x16_t acc[2][NT];
@@ -505,6 +719,14 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[m][i][r] = 0.f;
+  // Sums stay in accumulation registers: left to itself, the compiler moves some of
+  // them to others and back within the loop.
+  auto hold = [&] {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) asm volatile("" : "+a"(acc[m][i]));
+  };
   uint32_t frag[4];  // this lane's piece of row r32 for product j
 #pragma unroll
   for (int j = 0; j < 4; ++j) frag[j] = lds_addr(lds) + 128 * r32 + 16 * ((4 * h + j) ^ (r32 >> 1 & 7));
@@ -524,6 +746,7 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
   uint32_t place = 0;  // of this stage in the ring
   auto step = [&](auto oddc, int b) {
     constexpr bool odd = decltype(oddc)::value;
+    hold();
     // this stage has landed (what was requested since is the next ones), and every
     // wave is done with the one before, whose place is filled below
     if constexpr (!SG) twait<0>();
@@ -534,12 +757,12 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
     u32x4_t w[2][2], x[D + 1];
     uint32_t sw[2], sx[NT];
     const uint32_t sa = sfrag + (b / 2 & 1) * GB + (odd ? 8 : 0);
-    const uint32_t swa = sa + (PAIR ? 512 : 1024) * wave;
+    const uint32_t swa = sa + (PAIR ? 512 : 1024) * wn, sxa = sa + 512 * NT * wt;
     uint32_t fx[4], fw[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      fx[j] = frag[j] + place;
-      fw[j] = fx[j] + 8192 * wave;
+      fw[j] = frag[j] + place + 8192 * wn;
+      fx[j] = frag[j] + place + 4096 * NT * wt;
     }
     auto read_w = [&](auto jc) {
       constexpr int j = decltype(jc)::value;
@@ -552,7 +775,7 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
     };
     tread4<0>(swa, sw[0]);
     tread4<PAIR ? 2048 : 512>(swa, sw[1]);
-    static_for<NT>([&](auto ic) { tread4<TILE_COLS * 16 + 512 * decltype(ic)::value>(sa, sx[decltype(ic)::value]); });
+    static_for<NT>([&](auto ic) { tread4<TILE_COLS * 16 + 512 * decltype(ic)::value>(sxa, sx[decltype(ic)::value]); });
     read_w(std::integral_constant<int, 0>{});
     static_for<D>([&](auto fc) { read_x(fc); });
     const uint32_t out[2] = {past(b + ST - 1, piece[0]), past(b + ST - 1, piece[1])};
@@ -625,6 +848,7 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
   }
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   __syncthreads();  // LDS is free
+  hold();
 
   // A wave's 32 rows of a tile and their columns go through its part of LDS, so
   // that neighbouring lanes write neighbouring columns.
@@ -643,7 +867,7 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
           else v[q][k] = acc[m][i][4 * q + k];
         }
       if (PAIR && g.out_kind == MX4_OUT_MX4) {
-        const int nb = n0 + 32 * wave;  // a block of the result
+        const int nb = n0 + 32 * wn;  // a block of the result
         uint32_t top = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -662,7 +886,7 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
         const uint32_t mine = h ? q23 : q01, other = (uint32_t)__shfl_xor((int)(h ? q01 : q23), 32, 64);
         const uint32_t lo = h ? other : mine, hi = h ? mine : other;  // columns 8 q + 0..3 and 8 q + 4..7
         const u32x2_t o = {(lo & 0xFFFFu) | hi << 16, lo >> 16 | (hi & 0xFFFF0000u)};
-        const int r = 32 * i + r32;
+        const int r = 32 * (NT * wt + i) + r32;
         if (r < c.n && nb < g.N) {
           const long long p = c.row + r;
           *reinterpret_cast<u32x2_t *>(static_cast<uint8_t *>(g.out) + p * g.ldo + nb / 2 + 8 * h) = o;
@@ -674,11 +898,11 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
       }
     }
     if (PAIR && g.out_kind == MX4_OUT_MX4) continue;
-    const int rows = min(32, c.n - 32 * i), n = n0 + CW * wave + 4 * (lane % (CW / 4));
+    const int r0 = 32 * (NT * wt + i), rows = min(32, c.n - r0), n = n0 + CW * wn + 4 * (lane % (CW / 4));
 #pragma unroll 1
     for (int r = lane / (CW / 4); r < rows; r += 256 / CW) {
       f32x4_t v = *reinterpret_cast<const f32x4_t *>(turn + r * LD + 4 * (lane % (CW / 4)));
-      const long long p = c.row + 32 * i + r;
+      const long long p = c.row + r0 + r;
       if (partial != nullptr) {
         const int ldp = (g.N + 3) & ~3;
         if (n < g.N) *reinterpret_cast<f32x4_t *>(partial + p * ldp + n) = v;
@@ -692,7 +916,7 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
 }
 
 template <bool PAIR, bool SG>
-__global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4Args g, int splits, float *partial) {
+__global__ __launch_bounds__(512, 2) void mx4_tile_kernel(Mx4Args g, int splits, float *partial) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[TILE_LDS];
   const int nb = (g.N + (PAIR ? 127 : 255)) / (PAIR ? 128 : 256), pairs = (g.K + 511) / 512;
   const int chunks = g.chunks != nullptr ? *g.chunk_count : (g.P + TILE_ROWS - 1) / TILE_ROWS;
@@ -706,6 +930,7 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4Args g, int splits,
     nblk = item - ci * nb;
     const int4 v = g.chunks[ci];
     c = Chunk{v.x, v.y, v.z};
+    if (c.n <= 0) return;  // rounding to whole tiles left it none
   } else {
     // a few column tiles next to each other, then the next rows: what an XCD works
     // on at a time is near square
@@ -719,14 +944,11 @@ __global__ __launch_bounds__(256, 1) void mx4_tile_kernel(Mx4Args g, int splits,
   const int first = 2 * (int)((long long)split * pairs / splits);
   const int last = min(stages, 2 * (int)((long long)(split + 1) * pairs / splits));
   float *part = splits > 1 ? partial + (long long)split * g.P * ((g.N + 3) & ~3) : nullptr;
-  switch ((c.n + 31) / 32) {
+  switch ((c.n + 63) / 64) {
     case 1: mx4_tile<1, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
     case 2: mx4_tile<2, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
     case 3: mx4_tile<3, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
-    case 4: mx4_tile<4, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
-    case 5:
-    case 6: mx4_tile<6, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
-    default: mx4_tile<8, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
+    default: mx4_tile<4, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
   }
 }
 
@@ -744,17 +966,11 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args g, int splits, co
   store4<OUT>(g, t, n, v);
 }
 
-template <int NT, int NW, int U>
-void stream_by_type(const Mx4Args &g, int max_items, hipStream_t st) {
-  const dim3 gr((unsigned)std::min(max_items, 1 << 20)), blk(64 * NW);
-  if (g.w[1] != nullptr) {
-    if (g.out_kind == MX4_OUT_F32) hipLaunchKernelGGL((mx4_stream_kernel<NT, NW, U, true, MX4_OUT_F32>), gr, blk, 0, st, g);
-    else if (g.out_kind == MX4_OUT_BF16) hipLaunchKernelGGL((mx4_stream_kernel<NT, NW, U, true, MX4_OUT_BF16>), gr, blk, 0, st, g);
-    else hipLaunchKernelGGL((mx4_stream_kernel<NT, NW, U, true, MX4_OUT_MX4>), gr, blk, 0, st, g);
-  } else {
-    if (g.out_kind == MX4_OUT_F32) hipLaunchKernelGGL((mx4_stream_kernel<NT, NW, U, false, MX4_OUT_F32>), gr, blk, 0, st, g);
-    else hipLaunchKernelGGL((mx4_stream_kernel<NT, NW, U, false, MX4_OUT_BF16>), gr, blk, 0, st, g);
-  }
+template <int MAXT, bool PAIR, int KS>
+void launch_stream(const Mx4Args &g, long long groups, bool even, hipStream_t st) {
+  const dim3 gr((unsigned)((groups + 7) / 8 * 8)), blk(KS == 1 ? 256 : 512);
+  if (even) hipLaunchKernelGGL((mx4_stream_kernel<MAXT, PAIR, true, KS>), gr, blk, 0, st, g);
+  else hipLaunchKernelGGL((mx4_stream_kernel<MAXT, PAIR, false, KS>), gr, blk, 0, st, g);
 }
 
 constexpr long long PART_THREADS = 1LL << 31;  // a grid holds fewer than 2^32 threads
@@ -808,7 +1024,7 @@ bool scales_in_groups(const Mx4Args &g) {
   return ok(g.sx, g.ldsx) && ok(g.sw[0], g.K / 32) && (g.w[1] == nullptr || ok(g.sw[1], g.K / 32));
 }
 void launch_tiles(const Mx4Args &g, long long items, int splits, float *partial, hipStream_t st) {
-  const dim3 gr((unsigned)((items * splits + 7) / 8 * 8)), blk(256);
+  const dim3 gr((unsigned)((items * splits + 7) / 8 * 8)), blk(512);
   if (scales_in_groups(g)) {
     if (g.w[1] != nullptr) hipLaunchKernelGGL((mx4_tile_kernel<true, true>), gr, blk, 0, st, g, splits, partial);
     else hipLaunchKernelGGL((mx4_tile_kernel<false, true>), gr, blk, 0, st, g, splits, partial);
@@ -817,13 +1033,26 @@ void launch_tiles(const Mx4Args &g, long long items, int splits, float *partial,
     else hipLaunchKernelGGL((mx4_tile_kernel<false, false>), gr, blk, 0, st, g, splits, partial);
   }
 }
-int max_chunks(int E, int P, int rows) { return P / rows + std::min(E, P); }
-// parts of K where the tiles are fewer than the CUs, of two stages at least
+bool scales_in_pairs(const Mx4Args &g) {
+  auto ok = [](const uint8_t *p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 1) == 0 && ld % 2 == 0; };
+  return ok(g.sx, g.ldsx) && ok(g.sw[0], g.K / 32) && (g.w[1] == nullptr || ok(g.sw[1], g.K / 32));
+}
+// parts of K where the tiles are fewer than the CUs, of four stages at least
 int dense_splits(int T, int N, int K) {
   const long long tiles = (long long)((T + 255) / 256) * ((N + 255) / 256), pairs = (K + 511) / 512;
   return (int)std::max(1LL, std::min({256 / tiles, pairs, 16LL}));
 }
 bool dense_streams(int T) { return T <= 64; }
+
+// an expert's rows up to which its weights are streamed by waves of their own
+constexpr int FEW_ROWS_4 = 32;
+int few_chunks(int E, int P) { return std::min(E, P); }
+int many_chunks(int E, int P) { return P / TILE_ROWS + std::min(E, P / (FEW_ROWS_4 + 1)); }
+// work-groups of the stream kernel for a chunk
+int stream_groups(const Mx4Args &g) {
+  const int cols = g.w[1] != nullptr ? 64 : 128;
+  return (g.N + cols - 1) / cols;
+}
 }  // namespace
 
 size_t mx4_workspace_bytes(int T, int N, int K) {
@@ -833,10 +1062,12 @@ size_t mx4_workspace_bytes(int T, int N, int K) {
 }
 
 hipError_t launch_mx4_gemm(const Mx4Args &g, void *ws, hipStream_t st) {
-  const int nb = (g.N + 31) / 32;
   if (dense_streams(g.P)) {
-    if (g.P <= 16) stream_by_type<1, 8, 4>(g, nb, st);
-    else stream_by_type<4, 4, 2>(g, (g.P + 63) / 64 * nb, st);
+    const int nb = (g.N + 31) / 32;
+    const bool even = scales_in_pairs(g);
+    if (g.P <= 16) launch_stream<1, false, 8>(g, nb, even, st);
+    else if (g.P <= 32) launch_stream<2, false, 8>(g, nb, even, st);
+    else launch_stream<4, false, 8>(g, nb, even, st);
     return hipGetLastError();
   }
   const int splits = dense_splits(g.P, g.N, g.K);
@@ -851,21 +1082,37 @@ hipError_t launch_mx4_gemm(const Mx4Args &g, void *ws, hipStream_t st) {
   return hipGetLastError();
 }
 
-size_t mx4_expert_workspace_bytes(int E, int P, int, int) { return 256 + (size_t)max_chunks(E, P, 64) * sizeof(int4); }
+size_t mx4_expert_workspace_bytes(int E, int P, int, int) {
+  return 256 + (size_t)(few_chunks(E, P) + many_chunks(E, P)) * sizeof(int4);
+}
 
-hipError_t launch_mx4_expert(const Mx4Args &a, const int32_t *offsets, int E, void *ws, hipStream_t st) {
+hipError_t launch_mx4_expert(const Mx4Args &a, void *ws, hipStream_t st) {
   Mx4Args g = a;
+  const int E = g.n_experts, groups = stream_groups(g);
+  const bool pair = g.w[1] != nullptr, even = scales_in_pairs(g);
+  // few work-groups: they look for their chunks themselves, in place of a launch before
+  const int chunks = g.P / 64 + std::min(E, g.P);
+  if ((long long)chunks * groups <= 1024) {
+    if (pair) launch_stream<4, true, 1>(g, (long long)chunks * groups, even, st);
+    else launch_stream<4, false, 1>(g, (long long)chunks * groups, even, st);
+    return hipGetLastError();
+  }
   int32_t *count = static_cast<int32_t *>(ws);
-  int4 *chunks = reinterpret_cast<int4 *>(static_cast<char *>(ws) + 256);
-  const bool stream = g.P < 8 * E;
-  const int rows = stream ? 64 : TILE_ROWS, cap = max_chunks(E, g.P, rows);
-  hipLaunchKernelGGL(mx4_plan_kernel, dim3(1), dim3(1024), 0, st, offsets, E, g.P, rows, cap, chunks, count);
+  int4 *few = reinterpret_cast<int4 *>(static_cast<char *>(ws) + 256), *many = few + few_chunks(E, g.P);
+  hipLaunchKernelGGL(mx4_plan_kernel, dim3(1), dim3(1024), 0, st, g.offsets, E, g.P, FEW_ROWS_4, TILE_ROWS,
+                     few_chunks(E, g.P), few, count, many_chunks(E, g.P), many, count + 1);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  g.chunks = chunks;
+  if (many_chunks(E, g.P) > 0) {
+    g.chunks = many;
+    g.chunk_count = count + 1;
+    launch_tiles(g, (long long)many_chunks(E, g.P) * ((g.N + (pair ? 127 : 255)) / (pair ? 128 : 256)), 1, nullptr, st);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  g.chunks = few;
   g.chunk_count = count;
-  if (stream) stream_by_type<4, 4, 2>(g, cap * ((g.N + 31) / 32), st);
-  else launch_tiles(g, (long long)cap * ((g.N + (g.w[1] ? 127 : 255)) / (g.w[1] ? 128 : 256)), 1, nullptr, st);
+  if (pair) launch_stream<2, true, 1>(g, (long long)few_chunks(E, g.P) * groups, even, st);
+  else launch_stream<2, false, 1>(g, (long long)few_chunks(E, g.P) * groups, even, st);
   return hipGetLastError();
 }
 

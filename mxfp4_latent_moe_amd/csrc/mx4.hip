@@ -236,6 +236,11 @@ MOE_DEV void tread(uint32_t a, u32x4_t &v) {
   asm volatile("ds_read_b128 %0, %1 offset:%2" : "=&v"(v) : "v"(a), "n"(O) : "memory");
 }
 template <int O>
+MOE_DEV void tread2(uint32_t a, uint32_t &v) {
+  static_assert(O >= 0 && O < 65536, "offset field");
+  asm volatile("ds_read_u16 %0, %1 offset:%2" : "=&v"(v) : "v"(a), "n"(O) : "memory");
+}
+template <int O>
 MOE_DEV void tread4(uint32_t a, uint32_t &v) {
   static_assert(O >= 0 && O < 65536, "offset field");
   asm volatile("ds_read_b32 %0, %1 offset:%2" : "=&v"(v) : "v"(a), "n"(O) : "memory");
@@ -301,17 +306,27 @@ MOE_DEV bool find_chunk(const Mx4Args &g, int rows, int want, Chunk &c, int *lds
 // matrix) and 16 NT rows of x, and has a ring of its own in LDS, ST stages of 256
 // inputs, that direct loads of rows' whole 128 bytes fill: no wave waits for
 // another while it streams, and the waves of a CU keep some 100 KB on their way.
-// x and the scales come straight to registers, a stage ahead (the rows stay in the
-// L2).  KS waves of a work-group of NW share their columns and take parts of K;
-// their sums meet in LDS and are added in order.
+// x comes straight to registers, a stage ahead (the rows stay in the L2).  KS waves
+// of a work-group share their columns and take the stages of K in turn (at any time
+// they read a contiguous KS * 128 bytes of a row); their sums meet in LDS and are
+// added in order.
 //
 // In LDS piece p (16 bytes, a block) of row r lies at position p ^ (r / 2 % 8), as
 // the 16 rows that a quarter wave reads at once, two to a 256-byte line, then fall
 // on different banks.  Product j of a stage takes piece 2 kg + j from the lanes of
 // group kg (the groups' K need not be neighbours in memory), so that a lane's two
 // scale bytes of a stage are neighbours, of which the instruction selects one.
-// EVEN: scale rows are even distances apart, so that the two load as one.
-constexpr int STREAM_ST = 4, STREAM_STAGE = 32 * 128;
+//
+// Loads of two bytes a lane cost as much as those of sixteen.  With SG (scale rows
+// are whole dwords apart and aligned) the scales of two stages come into LDS by one
+// direct load for 32 rows, 16 bytes a row and stage; without it byte by byte to
+// registers.  7168 x 33792, 16 tokens: see stream_by_rows.
+constexpr int STREAM_STAGE = 32 * 128;
+constexpr int stream_st(int nt) { return nt == 1 ? 4 : 3; }
+constexpr int stream_group(int nt) { return 1024 + 512 * nt; }  // the weights' scales, then x's
+constexpr int STREAM_WAVE = 19 * 1024;  // LDS of a wave: the ring and two groups of scales
+constexpr bool stream_fits(int nt) { return stream_st(nt) * STREAM_STAGE + 2 * stream_group(nt) <= STREAM_WAVE; }
+static_assert(stream_fits(1) && stream_fits(2) && stream_fits(4), "LDS of a wave");
 
 // 16 bytes a lane straight into LDS (the host's pass over this code knows of 4 only)
 MOE_DEV void lds_load(__amdgpu_buffer_rsrc_t r, uint8_t *to, uint32_t voff, uint32_t soff) {
@@ -321,27 +336,23 @@ MOE_DEV void lds_load(__amdgpu_buffer_rsrc_t r, uint8_t *to, uint32_t voff, uint
 }
 
 // two neighbouring scale bytes
-template <bool EVEN>
 MOE_DEV uint32_t load_scales(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t at) {
-  if constexpr (EVEN) {
-    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, at, 0);
-  } else {
-    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b8(r, off, at, 0);
-    return lo | (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(r, off + 1, at, 0) << 8;
-  }
+  const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b8(r, off, at, 0);
+  return lo | (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(r, off + 1, at, 0) << 8;
 }
 
-// what a stage takes from registers: pieces of x, scales of x and of the weights
+// what a stage takes from registers: pieces of x, and without SG the scales
 template <int NT>
 struct StreamRegs {
   u32x4_t x[NT][2];
   uint32_t sx[NT], sw[2];
 };
 
-template <int NT, bool PAIR, bool EVEN, int KS>
+template <int NT, bool PAIR, bool SG, int KS>
 MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *lds) {
-  constexpr int ST = STREAM_ST, SB = STREAM_STAGE, DL = 4;
-  constexpr int RL = NT * (EVEN ? 3 : 4) + 2 * (EVEN ? 1 : 2);  // register loads of a stage
+  constexpr int ST = stream_st(NT), SB = STREAM_STAGE, GB = stream_group(NT), DL = 4;
+  constexpr int RL = SG ? 2 * NT : 4 * NT + 4;  // register loads of a stage
+  constexpr int GL = !SG ? 0 : (PAIR ? 2 : 1) + (NT == 4 ? 2 : 1);  // of a group of scales
   constexpr int CW = PAIR ? 16 : 32;
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, kg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -349,9 +360,9 @@ MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *ld
   const int n0 = CW * block, part = KS == 1 ? 0 : wave % KS;
   // a wave whose columns are past the last one only keeps the barriers whole
   const int nrows = __builtin_amdgcn_readfirstlane(max(min(CW, g.N - n0), 0));
-  const int first = (int)((long long)part * stages / KS);
-  const int count = nrows > 0 ? (int)((long long)(part + 1) * stages / KS) - first : 0;
-  uint8_t *const ring = lds + wave * (ST * SB);
+  // stage s of this wave is stage part + KS s of K
+  const int count = nrows > 0 ? (stages - part + KS - 1) / KS : 0;
+  uint8_t *const ring = lds + wave * STREAM_WAVE, *const groups = ring + ST * SB;
   constexpr uint32_t OUT = 0x80000000u;  // past the end of every buffer
 
   __amdgpu_buffer_rsrc_t wr[PAIR ? 2 : 1], sr[PAIR ? 2 : 1];
@@ -367,12 +378,25 @@ MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *ld
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(g.x + base * g.ldx, (uint32_t)((xrows - 1) * g.ldx + kbytes));
   const __amdgpu_buffer_rsrc_t xsr = make_rsrc(g.sx + base * g.ldsx, (uint32_t)((xrows - 1) * g.ldsx + kb));
   const int l8 = lane >> 3;
-  uint32_t piece[2], vw[DL], so[2], xo[NT], xso[NT];
+  uint32_t piece[2], vw[DL];
 #pragma unroll
   for (int q = 0; q < 2; ++q) piece[q] = 16 * ((lane & 7) ^ (4 * q + (lane >> 4)));
 #pragma unroll
   for (int u = 0; u < DL; ++u)  // 8 rows a load; the second matrix's are loads 2 and 3
     vw[u] = (uint32_t)(8 * (PAIR ? u & 1 : u) + l8) * (uint32_t)kbytes + piece[u & 1];
+  auto request = [&](int s) {  // stage s of this wave's part
+    uint8_t *const at = ring + (s % ST) * SB;
+    const uint32_t k0 = 128u * (part + KS * s);
+    // of a stage that ends inside, pieces past K read out of range: zeros
+    const uint32_t past[2] = {k0 + piece[0] < (uint32_t)kbytes ? 0u : OUT, k0 + piece[1] < (uint32_t)kbytes ? 0u : OUT};
+#pragma unroll
+    for (int u = 0; u < DL; ++u)
+      lds_load(wr[PAIR ? u >> 1 : 0], at + 1024 * u, vw[u] | past[u & 1], k0);
+  };
+  // the weights go out before anything about x's rows is known
+  for (int s = 0; s < min(ST - 1, count); ++s) request(s);
+
+  uint32_t so[2], xo[NT], xso[NT];
 #pragma unroll
   for (int m = 0; m < 2; ++m) so[m] = (uint32_t)min((PAIR ? 0 : 16 * m) + r16, nrows - 1) * (uint32_t)kb + 2 * kg;
 #pragma unroll
@@ -383,28 +407,45 @@ MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *ld
     xo[i] = in ? r * (uint32_t)g.ldx + 32 * kg : OUT;
     xso[i] = in ? r * (uint32_t)g.ldsx + 2 * kg : OUT;
   }
-
-  auto request = [&](int s) {  // stage s of this wave's part
-    uint8_t *const at = ring + (s % ST) * SB;
-    const uint32_t k0 = 128u * (first + s);
-    // of a stage that ends inside, pieces past K read out of range: zeros
-    const uint32_t past[2] = {k0 + piece[0] < (uint32_t)kbytes ? 0u : OUT, k0 + piece[1] < (uint32_t)kbytes ? 0u : OUT};
-#pragma unroll
-    for (int u = 0; u < DL; ++u)
-      lds_load(wr[PAIR ? u >> 1 : 0], at + 1024 * u, vw[u] | past[u & 1], k0);
-  };
   using Regs = StreamRegs<NT>;
   auto load = [&](Regs &v, int s) {
-    const uint32_t k0 = 128u * (first + s), b0 = 8u * (first + s);
+    const uint32_t k0 = 128u * (part + KS * s), b0 = 8u * (part + KS * s);
     const uint32_t past = b0 + 2 * kg < (uint32_t)kb ? 0u : OUT, past2 = b0 + 2 * kg + 1 < (uint32_t)kb ? 0u : OUT;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       v.x[i][0] = buf_load16(xr, xo[i] | past, k0);
       v.x[i][1] = buf_load16(xr, (xo[i] + 16) | past2, k0);
-      v.sx[i] = load_scales<EVEN>(xsr, xso[i] | past, b0);
+      if constexpr (!SG) v.sx[i] = load_scales(xsr, xso[i] | past, b0);
     }
+    if constexpr (!SG) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m) v.sw[m] = load_scales<EVEN>(sr[PAIR ? m : 0], so[m] | past, b0);
+      for (int m = 0; m < 2; ++m) v.sw[m] = load_scales(sr[PAIR ? m : 0], so[m] | past, b0);
+    }
+  };
+  // scales of stages 2 q and 2 q + 1, [stage][row][16], of a pair the one matrix's and
+  // then the other's; a row's bytes past its end are others'
+  uint32_t vg = 0, vgx[2] = {0, 0};
+  if constexpr (SG) {
+    vg = (uint32_t)min(PAIR ? r16 : lane & 31, max(nrows - 1, 0)) * (uint32_t)kb + 8 * KS * (PAIR ? lane >> 4 : lane >> 5);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = NT == 4 ? lane : lane % (16 * NT), later = NT == 4 ? q : lane / (16 * NT);
+      vgx[q] = r < c.n && later < 2 ? (uint32_t)(x_row(g, c.row + r) - (int)base) * (uint32_t)g.ldsx + 8 * KS * later : OUT;
+    }
+  }
+  auto request_scales = [&](int q) {
+    if constexpr (SG) {
+      uint8_t *const at = groups + (q & 1) * GB;
+      const uint32_t b0 = 8u * (part + KS * 2 * q);
+      if constexpr (PAIR) {  // half a wave's lanes for each matrix
+        if (lane < 32) lds_load(sr[0], at, vg, b0);
+        if (lane < 32) lds_load(sr[PAIR ? 1 : 0], at + 512, vg, b0);
+      } else {
+        lds_load(sr[0], at, vg, b0);
+      }
+      if (NT > 1 || lane < 32) lds_load(xsr, at + 1024, vgx[0], b0);
+      if constexpr (NT == 4) lds_load(xsr, at + 2048, vgx[1], b0);
+    }
   };
 
   f32x4_t acc[2][NT];
@@ -415,32 +456,56 @@ MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *ld
   uint32_t frag[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) frag[j] = lds_addr(ring) + 128 * r16 + 16 * ((2 * kg + j) ^ (r16 >> 1));
-  auto step = [&](auto morec, int s, Regs &now, Regs &next) {
-    constexpr bool more = decltype(morec)::value;  // a stage is left to request
+  const uint32_t sfrag = lds_addr(groups) + 16 * r16 + 2 * kg;
+  // In the order of their requests: registers of stage s, at even s the scales of
+  // s + 2 and s + 3, stage s + ST - 1.  MORE: such a stage is left; else `more` says so.
+  auto step = [&](auto oddc, auto morec, bool more, int s, Regs &now, Regs &next) {
+    constexpr bool odd = decltype(oddc)::value, MORE = decltype(morec)::value;
     load(next, min(s + 1, count - 1));
     __builtin_amdgcn_sched_barrier(0);  // the waits count loads in this order
-    if constexpr (more) request(s + ST - 1);
-    // this stage and its registers have landed; requested since are the next two
-    // stages and the next registers (near the end at most the registers)
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm((more ? DL * (ST - 2) : 0) + RL));
+    if (!odd && (MORE || s + 2 < count)) request_scales(s / 2 + 1);
+    // this stage, its registers and scales have landed; requested since are later ones'
+    if (MORE || more) {
+      request(s + ST - 1);
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(DL * (ST - 2) + RL + (odd ? 0 : GL)));
+    } else {
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(RL));  // near the end fewer are on their way
+    }
     __builtin_amdgcn_sched_barrier(0);
     const uint32_t at = (s % ST) * SB;
     u32x4_t w[2][2];
+    uint32_t sw[2], sx[NT];
+    if constexpr (SG) {
+      const uint32_t sa = sfrag + (s / 2 & 1) * GB, swa = sa + (odd ? PAIR ? 256 : 512 : 0), sxa = sa + 1024 + (odd ? 256 * NT : 0);
+      tread2<0>(swa, sw[0]);
+      tread2<PAIR ? 512 : 256>(swa, sw[1]);
+      static_for<NT>([&](auto ic) { tread2<256 * decltype(ic)::value>(sxa, sx[decltype(ic)::value]); });
+    } else {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) sw[m] = now.sw[m];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) sx[i] = now.sx[i];
+    }
     tread<0>(frag[0] + at, w[0][0]);
     tread<2048>(frag[0] + at, w[1][0]);
     tread<0>(frag[1] + at, w[0][1]);
     tread<2048>(frag[1] + at, w[1][1]);
     // scale bytes past K are of other rows: one in their place
-    const int in = kb - 8 * (first + s) - 2 * kg;
+    const int in = kb - 8 * (part + KS * s) - 2 * kg;
     const uint32_t mask = in >= 2 ? 0xFFFFu : in <= 0 ? 0u : 0xFFu;
-    uint32_t sw[2], sx[NT];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) sw[m] = (now.sw[m] & mask) | (0x7F7Fu & ~mask);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) sx[i] = (now.sx[i] & mask) | (0x7F7Fu & ~mask);
     twait<2>();
     ttie(w[0][0]);
     ttie(w[1][0]);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if constexpr (SG) ttie(sw[m]);
+      sw[m] = (sw[m] & mask) | (0x7F7Fu & ~mask);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if constexpr (SG) ttie(sx[i]);
+      sx[i] = (sx[i] & mask) | (0x7F7Fu & ~mask);
+    }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -454,34 +519,24 @@ MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *ld
       for (int i = 0; i < NT; ++i) acc[m][i] = mfma_4_16<1>(w[m][1], now.x[i][1], acc[m][i], sw[m], sx[i]);
   };
   if (count > 0) {
+    const std::false_type even;
+    const std::true_type odd;
     Regs a, b;
+    request_scales(0);
     load(a, 0);
-    for (int s = 0; s < min(ST - 1, count); ++s) request(s);
-    auto turn = [&] {  // the next registers become these
-#pragma unroll
-      for (int m = 0; m < 2; ++m) a.sw[m] = b.sw[m];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        a.sx[i] = b.sx[i];
-        a.x[i][0] = b.x[i][0];
-        a.x[i][1] = b.x[i][1];
-      }
-    };
-    const std::integral_constant<bool, true> more;
-    const std::integral_constant<bool, false> none;
-    const int most = count - (ST - 1);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // the first stages went out in another order than the rest
+    __builtin_amdgcn_sched_barrier(0);
+    const int most = count - (ST - 1);  // steps that request a stage
     int s = 0;
     for (; s + 1 < most; s += 2) {
-      step(more, s, a, b);
-      step(more, s + 1, b, a);
+      step(even, std::true_type{}, true, s, a, b);
+      step(odd, std::true_type{}, true, s + 1, b, a);
     }
-    if (s < most) {
-      step(more, s++, a, b);
-      turn();
-    }
-    for (; s < count; ++s) {
-      step(none, s, a, b);
-      turn();
+    for (;;) {  // s is even
+      step(even, std::false_type{}, s < most, s, a, b);
+      if (++s >= count) break;
+      step(odd, std::false_type{}, s < most, s, b, a);
+      if (++s >= count) break;
     }
   }
 
@@ -498,7 +553,7 @@ MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *ld
     for (int t = part; t < 2 * NT; t += KS) {
       f32x4_t v = {0.f, 0.f, 0.f, 0.f};
       for (int q = 0; q < KS; ++q)
-        v += reinterpret_cast<const f32x4_t *>(lds + (w0 + q) * (ST * SB))[64 * t + lane];
+        v += reinterpret_cast<const f32x4_t *>(lds + (w0 + q) * STREAM_WAVE)[64 * t + lane];
       const int m = t / NT, r = 16 * (t % NT) + r16, n = n0 + 16 * m + 4 * kg;
       if (r < c.n) {
         if (g.out_kind == MX4_OUT_BF16) store4<MX4_OUT_BF16>(g, c.row + r, n, v);
@@ -553,19 +608,19 @@ MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *ld
   }
 }
 
-template <int MAXT, bool PAIR, bool EVEN, int KS>
+template <int MAXT, bool PAIR, bool SG, int KS>
 MOE_DEV void mx4_stream_rows(const Mx4Args &g, const Chunk &c, int block, uint8_t *lds) {
-  if (MAXT == 1 || c.n <= 16) mx4_stream<1, PAIR, EVEN, KS>(g, c, block, lds);
-  else if (MAXT == 2 || c.n <= 32) mx4_stream<(MAXT < 2 ? MAXT : 2), PAIR, EVEN, KS>(g, c, block, lds);
-  else mx4_stream<MAXT, PAIR, EVEN, KS>(g, c, block, lds);
+  if (MAXT == 1 || c.n <= 16) mx4_stream<1, PAIR, SG, KS>(g, c, block, lds);
+  else if (MAXT == 2 || c.n <= 32) mx4_stream<(MAXT < 2 ? MAXT : 2), PAIR, SG, KS>(g, c, block, lds);
+  else mx4_stream<MAXT, PAIR, SG, KS>(g, c, block, lds);
 }
 
 // work-groups of 4 waves with a block of columns each, two on a CU (grouped), or of
 // 8 that share one (dense); chunks of at most 16 MAXT rows
-template <int MAXT, bool PAIR, bool EVEN, int KS>
+template <int MAXT, bool PAIR, bool SG, int KS>
 __global__ __launch_bounds__(KS == 1 ? 256 : 512, 2) void mx4_stream_kernel(Mx4Args g) {
   constexpr int NW = KS == 1 ? 4 : 8, BLOCKS = NW / KS;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * STREAM_ST * STREAM_STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NW * STREAM_WAVE];
   const int nb = ((g.N + (PAIR ? 15 : 31)) / (PAIR ? 16 : 32) + BLOCKS - 1) / BLOCKS;  // work-groups a chunk
   Chunk c;
   int nblk;
@@ -593,7 +648,7 @@ __global__ __launch_bounds__(KS == 1 ? 256 : 512, 2) void mx4_stream_kernel(Mx4A
   // the same in every lane, which buffer descriptors need
   c = Chunk{__builtin_amdgcn_readfirstlane(c.expert), __builtin_amdgcn_readfirstlane(c.row),
             __builtin_amdgcn_readfirstlane(c.n)};
-  mx4_stream_rows<MAXT, PAIR, EVEN, KS>(g, c, block, lds);
+  mx4_stream_rows<MAXT, PAIR, SG, KS>(g, c, block, lds);
 }
 
 // ---- many rows
@@ -670,11 +725,6 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
     const int n = 32 * (PAIR ? wave >> 1 : wave) + 8 * u + l8;  // of a pair, even waves the first matrix's rows
     vw[u] = (uint32_t)n * (uint32_t)kbytes + piece[u & 1];
   }
-#pragma unroll
-  for (int u = 0; u < XL; ++u) {
-    const int r = 8 * (8 * u + wave) + l8;
-    vx[u] = r < c.n ? row_of(r) * (uint32_t)g.ldx + piece[wave & 1] : OUT;
-  }
   // what to add where stage b ends inside; stages after the last are read as the last, unused
   auto past = [&](int b, uint32_t p) { return 128u * (first + min(b, count - 1)) + p < (uint32_t)kbytes ? 0u : OUT; };
   // load u of stage b, to the place at `place` of the ring
@@ -689,6 +739,17 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           xr, (lds_void *)(at + (TILE_COLS + 8 * (8 * (u - WL) + wave)) * 128), 16, vx[u - WL] | out[wave & 1], k0, 0, 0);
   };
+  // the first stages' weights go out before anything about x's rows is known
+  static_for<ST - 1>([&](auto sc) {
+    constexpr int s = decltype(sc)::value;
+    const uint32_t out[2] = {past(s, piece[0]), past(s, piece[1])};
+    static_for<WL>([&](auto uc) { request(s * SB, s, out, uc); });
+  });
+#pragma unroll
+  for (int u = 0; u < XL; ++u) {
+    const int r = 8 * (8 * u + wave) + l8;
+    vx[u] = r < c.n ? row_of(r) * (uint32_t)g.ldx + piece[wave & 1] : OUT;
+  }
   // scales of stages 2 q and 2 q + 1: [row][16], a row a lane; waves 0 to 3 the
   // weights' (of a pair first one matrix's 128 rows, then the other's), the others x's
   const int sr_row = 64 * (PAIR && wt == 0 ? wn & 1 : wn) + lane;
@@ -712,6 +773,16 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
     if constexpr (!SG) reinterpret_cast<u32x4_t *>(groups + (q & 1) * GB)[tid] = held;
   };
 
+  request_scales(0);
+  static_for<ST - 1>([&](auto sc) {
+    constexpr int s = decltype(sc)::value;
+    const uint32_t out[2] = {past(s, piece[0]), past(s, piece[1])};
+    static_for<XL>([&](auto uc) { request(s * SB, s, out, std::integral_constant<int, WL + decltype(uc)::value>{}); });
+  });
+  put_scales(0);
+  // they went out in another order than the rest (of two stages, the first step waits for all)
+  if constexpr (ST > 2) __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+
   f32x16_t acc[2][NT];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -732,13 +803,6 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
   for (int j = 0; j < 4; ++j) frag[j] = lds_addr(lds) + 128 * r32 + 16 * ((4 * h + j) ^ (r32 >> 1 & 7));
   const uint32_t sfrag = lds_addr(groups) + 16 * r32 + 4 * h;
 
-  request_scales(0);
-  put_scales(0);
-  static_for<ST - 1>([&](auto sc) {
-    constexpr int s = decltype(sc)::value;
-    const uint32_t out[2] = {past(s, piece[0]), past(s, piece[1])};
-    static_for<WL + XL>([&](auto uc) { request(s * SB, s, out, uc); });
-  });
   // the order of a stage's LDS reads: the scales, the first product's weights and D
   // rows' pieces; then with each tile the rows' piece D tiles on, and with a
   // product's first tile the next product's weights
@@ -966,10 +1030,15 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args g, int splits, co
   store4<OUT>(g, t, n, v);
 }
 
+// scale rows that can be loaded 16 bytes at a time
+bool scales_in_groups(const Mx4Args &g) {
+  auto ok = [](const uint8_t *p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && ld % 4 == 0; };
+  return ok(g.sx, g.ldsx) && ok(g.sw[0], g.K / 32) && (g.w[1] == nullptr || ok(g.sw[1], g.K / 32));
+}
 template <int MAXT, bool PAIR, int KS>
-void launch_stream(const Mx4Args &g, long long groups, bool even, hipStream_t st) {
+void launch_stream(const Mx4Args &g, long long groups, hipStream_t st) {
   const dim3 gr((unsigned)((groups + 7) / 8 * 8)), blk(KS == 1 ? 256 : 512);
-  if (even) hipLaunchKernelGGL((mx4_stream_kernel<MAXT, PAIR, true, KS>), gr, blk, 0, st, g);
+  if (scales_in_groups(g)) hipLaunchKernelGGL((mx4_stream_kernel<MAXT, PAIR, true, KS>), gr, blk, 0, st, g);
   else hipLaunchKernelGGL((mx4_stream_kernel<MAXT, PAIR, false, KS>), gr, blk, 0, st, g);
 }
 
@@ -1018,11 +1087,6 @@ hipError_t launch_dequantize4(const uint8_t *q, long long ldq, const uint8_t *qs
 }
 
 namespace {
-// scale rows that can be loaded 16 bytes at a time
-bool scales_in_groups(const Mx4Args &g) {
-  auto ok = [](const uint8_t *p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0 && ld % 4 == 0; };
-  return ok(g.sx, g.ldsx) && ok(g.sw[0], g.K / 32) && (g.w[1] == nullptr || ok(g.sw[1], g.K / 32));
-}
 void launch_tiles(const Mx4Args &g, long long items, int splits, float *partial, hipStream_t st) {
   const dim3 gr((unsigned)((items * splits + 7) / 8 * 8)), blk(512);
   if (scales_in_groups(g)) {
@@ -1032,10 +1096,6 @@ void launch_tiles(const Mx4Args &g, long long items, int splits, float *partial,
     if (g.w[1] != nullptr) hipLaunchKernelGGL((mx4_tile_kernel<true, false>), gr, blk, 0, st, g, splits, partial);
     else hipLaunchKernelGGL((mx4_tile_kernel<false, false>), gr, blk, 0, st, g, splits, partial);
   }
-}
-bool scales_in_pairs(const Mx4Args &g) {
-  auto ok = [](const uint8_t *p, long long ld) { return (reinterpret_cast<uintptr_t>(p) & 1) == 0 && ld % 2 == 0; };
-  return ok(g.sx, g.ldsx) && ok(g.sw[0], g.K / 32) && (g.w[1] == nullptr || ok(g.sw[1], g.K / 32));
 }
 // parts of K where the tiles are fewer than the CUs, of four stages at least
 int dense_splits(int T, int N, int K) {
@@ -1064,10 +1124,9 @@ size_t mx4_workspace_bytes(int T, int N, int K) {
 hipError_t launch_mx4_gemm(const Mx4Args &g, void *ws, hipStream_t st) {
   if (dense_streams(g.P)) {
     const int nb = (g.N + 31) / 32;
-    const bool even = scales_in_pairs(g);
-    if (g.P <= 16) launch_stream<1, false, 8>(g, nb, even, st);
-    else if (g.P <= 32) launch_stream<2, false, 8>(g, nb, even, st);
-    else launch_stream<4, false, 8>(g, nb, even, st);
+    if (g.P <= 16) launch_stream<1, false, 8>(g, nb, st);
+    else if (g.P <= 32) launch_stream<2, false, 8>(g, nb, st);
+    else launch_stream<4, false, 8>(g, nb, st);
     return hipGetLastError();
   }
   const int splits = dense_splits(g.P, g.N, g.K);
@@ -1089,12 +1148,12 @@ size_t mx4_expert_workspace_bytes(int E, int P, int, int) {
 hipError_t launch_mx4_expert(const Mx4Args &a, void *ws, hipStream_t st) {
   Mx4Args g = a;
   const int E = g.n_experts, groups = stream_groups(g);
-  const bool pair = g.w[1] != nullptr, even = scales_in_pairs(g);
+  const bool pair = g.w[1] != nullptr;
   // few work-groups: they look for their chunks themselves, in place of a launch before
   const int chunks = g.P / 64 + std::min(E, g.P);
   if ((long long)chunks * groups <= 1024) {
-    if (pair) launch_stream<4, true, 1>(g, (long long)chunks * groups, even, st);
-    else launch_stream<4, false, 1>(g, (long long)chunks * groups, even, st);
+    if (pair) launch_stream<4, true, 1>(g, (long long)chunks * groups, st);
+    else launch_stream<4, false, 1>(g, (long long)chunks * groups, st);
     return hipGetLastError();
   }
   int32_t *count = static_cast<int32_t *>(ws);
@@ -1111,8 +1170,8 @@ hipError_t launch_mx4_expert(const Mx4Args &a, void *ws, hipStream_t st) {
   }
   g.chunks = few;
   g.chunk_count = count;
-  if (pair) launch_stream<2, true, 1>(g, (long long)few_chunks(E, g.P) * groups, even, st);
-  else launch_stream<2, false, 1>(g, (long long)few_chunks(E, g.P) * groups, even, st);
+  if (pair) launch_stream<2, true, 1>(g, (long long)few_chunks(E, g.P) * groups, st);
+  else launch_stream<2, false, 1>(g, (long long)few_chunks(E, g.P) * groups, st);
   return hipGetLastError();
 }
 

@@ -521,7 +521,8 @@ int moe_mxfp4_dequantize(int T, int K, const uint8_t *q, int64_t ldq, const uint
  * bytes are 0..254; 255 gives NaN in its row or column.  Where the product of a
  * block's two scales leaves fp32's range the result is unspecified.
  * Deterministic.  T may be 0; N is free; K is a multiple of 32 (else
- * MOE_ENOTSUP; T up to 2^21, N and K up to 2^20, ldx and ldxs up to 2^22).
+ * MOE_ENOTSUP; T up to 2^21, N and K up to 2^20, T * N up to 2^33, ldx and ldxs up
+ * to 2^22).
  * Workspace: moe_mxfp4_gemm_workspace_bytes(T, N, K) bytes (0: unsupported).
  * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */
 size_t moe_mxfp4_gemm_workspace_bytes(int T, int N, int K);
@@ -560,8 +561,9 @@ typedef struct {
  * rows cost nothing; nothing waits on the host.  Device preconditions:
  * ascending offsets from 0 to at most P, sorted_pair[p] / top_k in [0, x_rows).
  * Deterministic.  Limits (else MOE_ENOTSUP): K a multiple of 32, N too with
- * MOE_DT_MXFP4; at most 1024 experts; P up to 2^21, N and K up to 2^20, ldx and
- * ldxs up to 2^22; gathered, x_rows * ldx and x_rows * ldxs below 2^31.  P may
+ * MOE_DT_MXFP4; at most 1024 experts; P up to 2^21, N up to 2^18, K up to 2^20, P *
+ * N up to 2^33, ldx and ldxs up to 2^22; gathered, x_rows * ldx and x_rows * ldxs
+ * below 2^31.  P may
  * be 0.  Workspace: moe_mxfp4_expert_gemm_workspace_bytes(E, P, N, K) bytes (0:
  * unsupported).
  * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */

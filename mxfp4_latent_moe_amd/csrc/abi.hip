@@ -564,15 +564,23 @@ static int mxfp4_dequantize_impl(int T, int K, const uint8_t *q, int64_t ldq, co
 }
 
 // limits of the products' kernels: whole blocks, 32-bit offsets within the rows
-// one work-group reads, and a count of work items in 32 bits
+// one work-group reads, and a grid of fewer than 2^32 threads
 static int mxfp4_check_sizes(int P, int N, int K) {
   if (P < 0 || N <= 0 || K <= 0) return MOE_EINVAL;
-  if (K % 32 || K > (1 << 20) || P > (1 << 21) || N > (1 << 20)) return MOE_ENOTSUP;
+  if (K % 32 || K > (1 << 20) || P > (1 << 21) || N > (1 << 20) || (long long)P * N > (1LL << 33)) return MOE_ENOTSUP;
   return MOE_OK;
 }
-static bool rows_vec(const void *p, long long ld, int dtype) {
-  const size_t piece = dtype == MOE_DT_BF16 ? 8 : 16;
-  return aligned(p, piece) && (ld * (long long)dtype_bytes(dtype)) % (long long)piece == 0;
+static int mxfp4_check_experts(int E, int P, int N, int K) {
+  if (E <= 0) return MOE_EINVAL;
+  const int rc = mxfp4_check_sizes(P, N, K);
+  if (rc) return rc;
+  return E > MX4_MAX_E || N > (1 << 18) ? MOE_ENOTSUP : MOE_OK;
+}
+// how rows of the result can be written: 16 bytes at a time, bf16 8, value by value
+static int rows_vec(const void *p, long long ld, int dtype) {
+  const long long bytes = ld * (long long)dtype_bytes(dtype);
+  if (aligned16(p) && bytes % 16 == 0) return 2;
+  return dtype == MOE_DT_BF16 && aligned(p, 8) && bytes % 8 == 0;
 }
 
 static int mxfp4_gemm_impl(int T, int N, int K, const uint8_t *x, int64_t ldx, const uint8_t *x_scale, int64_t ldxs,
@@ -609,9 +617,9 @@ static int mxfp4_gemm_impl(int T, int N, int K, const uint8_t *x, int64_t ldx, c
 }
 
 static int mxfp4_expert_impl(const moe_mxfp4_expert_args *a, void *ws, size_t ws_bytes, void *stream) {
-  if (!a || a->n_experts <= 0) return MOE_EINVAL;
+  if (!a) return MOE_EINVAL;
   const int P = a->P, N = a->N, K = a->K;
-  int rc = mxfp4_check_sizes(P, N, K);
+  int rc = mxfp4_check_experts(a->n_experts, P, N, K);
   if (rc) return rc;
   const bool pair = a->w3 != nullptr, four = a->out_dtype == MOE_DT_MXFP4;
   if (!a->expert_offsets || !a->x || !a->x_scale || !a->w || !a->w_scale || !a->out || !ws) return MOE_EINVAL;
@@ -630,7 +638,7 @@ static int mxfp4_expert_impl(const moe_mxfp4_expert_args *a, void *ws, size_t ws
   } else if (a->ldo < N || !aligned(a->out, dtype_bytes(a->out_dtype))) {
     return MOE_EINVAL;
   }
-  if (a->n_experts > MX4_MAX_E || a->ldx > (1 << 22) || a->ldxs > (1 << 22)) return MOE_ENOTSUP;
+  if (a->ldx > (1 << 22) || a->ldxs > (1 << 22)) return MOE_ENOTSUP;
   // gathered rows are addressed with 32 bits from the first one
   if (gathered && (long long)a->x_rows * a->ldx >= (1LL << 31)) return MOE_ENOTSUP;
   if (gathered && (long long)a->x_rows * a->ldxs >= (1LL << 31)) return MOE_ENOTSUP;
@@ -658,7 +666,7 @@ static int mxfp4_expert_impl(const moe_mxfp4_expert_args *a, void *ws, size_t ws
   g.os = a->out_scale;
   g.ldos = a->ldos;
   g.out_kind = four ? MX4_OUT_MX4 : a->out_dtype == MOE_DT_BF16 ? MX4_OUT_BF16 : MX4_OUT_F32;
-  g.vec_out = !four && rows_vec(a->out, a->ldo, a->out_dtype);
+  g.vec_out = four ? 0 : rows_vec(a->out, a->ldo, a->out_dtype);
   g.P = P;
   g.N = N;
   g.K = K;
@@ -1335,7 +1343,7 @@ int moe_mxfp4_gemm(int T, int N, int K, const uint8_t *x, int64_t ldx, const uin
 }
 
 size_t moe_mxfp4_expert_gemm_workspace_bytes(int E, int P, int N, int K) {
-  if (E <= 0 || E > MX4_MAX_E || mxfp4_check_sizes(P, N, K) != MOE_OK) return 0;
+  if (mxfp4_check_experts(E, P, N, K) != MOE_OK) return 0;
   return ALIGN + align_up(mx4_expert_workspace_bytes(E, P, N, K));
 }
 

@@ -249,7 +249,7 @@ struct Mx4Args {
   uint8_t *os;            // MX4_OUT_MX4: scale bytes
   long long ldos;
   int out_kind, accumulate;
-  int vec_out;            // rows of out are 16-byte (bf16: 8-byte) aligned
+  int vec_out;            // rows of out are 16-byte aligned: 2; of bf16 8-byte: 1
   int P, N, K;
   const int32_t *offsets; // grouped: expert e's rows are offsets[e] .. offsets[e + 1] (NULL: dense)
   int n_experts;

@@ -11,6 +11,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "mx4_plan.h"
 #include "quant4.h"
 
 namespace moe {
@@ -320,7 +321,7 @@ MOE_DEV bool find_chunk(const Mx4Args &g, int rows, int want, Chunk &c, int *lds
 // Loads of two bytes a lane cost as much as those of sixteen.  With SG (scale rows
 // are whole dwords apart and aligned) the scales of two stages come into LDS by one
 // direct load for 32 rows, 16 bytes a row and stage; without it byte by byte to
-// registers.  7168 x 33792, 16 tokens: see stream_by_rows.
+// registers.  7168 x 33792: one token 25 us, 16 tokens 31
 constexpr int STREAM_STAGE = 32 * 128;
 constexpr int stream_st(int nt) { return nt == 1 ? 4 : 3; }
 constexpr int stream_group(int nt) { return 1024 + 512 * nt; }  // the weights' scales, then x's
@@ -962,57 +963,101 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
       }
     }
     if (PAIR && g.out_kind == MX4_OUT_MX4) continue;
-    const int r0 = 32 * (NT * wt + i), rows = min(32, c.n - r0), n = n0 + CW * wn + 4 * (lane % (CW / 4));
-#pragma unroll 1
-    for (int r = lane / (CW / 4); r < rows; r += 256 / CW) {
-      f32x4_t v = *reinterpret_cast<const f32x4_t *>(turn + r * LD + 4 * (lane % (CW / 4)));
-      const long long p = c.row + r0 + r;
-      if (partial != nullptr) {
-        const int ldp = (g.N + 3) & ~3;
-        if (n < g.N) *reinterpret_cast<f32x4_t *>(partial + p * ldp + n) = v;
-        continue;
-      }
-      if (!PAIR && g.pair_weight != nullptr) v *= g.pair_weight[g.pair[p]];
-      if (g.out_kind == MX4_OUT_BF16) store4<MX4_OUT_BF16>(g, p, n, v);
-      else store4<MX4_OUT_F32>(g, p, n, v);
+    const int r0 = 32 * (NT * wt + i);
+    // W columns a lane and a row of the tile every CW / W lanes
+    auto rows = [&](auto wc, auto &&put) {
+      constexpr int W = decltype(wc)::value, RS = 64 * W / CW;
+      const int rl = lane / (CW / W), nl = W * (lane % (CW / W));
+      f32x4_t v[32 / RS][W / 4];
+#pragma unroll
+      for (int q = 0; q < 32 / RS; ++q)
+#pragma unroll
+        for (int k = 0; k < W / 4; ++k) v[q][k] = *reinterpret_cast<const f32x4_t *>(turn + (rl + RS * q) * LD + nl + 4 * k);
+#pragma unroll
+      for (int q = 0; q < 32 / RS; ++q)
+        if (r0 + rl + RS * q < c.n) put(c.row + r0 + rl + RS * q, n0 + CW * wn + nl, v[q]);
+    };
+    if (partial != nullptr) {
+      const int ldp = (g.N + 3) & ~3;
+      rows(std::integral_constant<int, 4>{}, [&](long long p, int n, f32x4_t(&v)[1]) {
+        if (n < g.N) *reinterpret_cast<f32x4_t *>(partial + p * ldp + n) = v[0];
+      });
+    } else if (g.out_kind == MX4_OUT_BF16) {
+      rows(std::integral_constant<int, 8>{}, [&](long long p, int n, f32x4_t(&v)[2]) {
+        if (!PAIR && g.pair_weight != nullptr) {
+          const float pw = g.pair_weight[g.pair[p]];
+          v[0] *= pw;
+          v[1] *= pw;
+        }
+        if (g.vec_out == 2 && n + 7 < g.N) {
+          bf16x8_t b;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) b[k] = to_bf16(v[k >> 2][k & 3]);
+          *reinterpret_cast<bf16x8_t *>(static_cast<__bf16 *>(g.out) + p * g.ldo + n) = b;
+        } else {
+          store4<MX4_OUT_BF16>(g, p, n, v[0]);
+          store4<MX4_OUT_BF16>(g, p, n + 4, v[1]);
+        }
+      });
+    } else {
+      rows(std::integral_constant<int, 4>{}, [&](long long p, int n, f32x4_t(&v)[1]) {
+        if (!PAIR && g.pair_weight != nullptr) v[0] *= g.pair_weight[g.pair[p]];
+        store4<MX4_OUT_F32>(g, p, n, v[0]);
+      });
     }
   }
 }
 
+// block -> item of `total`, as xcd_logical
+MOE_DEV int tile_of(int block, int total) {
+  const int t8 = (total + 7) & ~7, id = (block & 7) * (t8 >> 3) + (block >> 3);
+  return block < t8 && id < total ? id : -1;
+}
+
+// grouped: an item is a chunk and a tile of columns.  Dense: tiles of 256 rows for
+// the first `cut` column tiles, of `rows` for the others, whose K may be split
 template <bool PAIR, bool SG>
-__global__ __launch_bounds__(512, 2) void mx4_tile_kernel(Mx4Args g, int splits, float *partial) {
+__global__ __launch_bounds__(512, 2) void mx4_tile_kernel(Mx4Args g, int rows, int cut, int splits, float *partial) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[TILE_LDS];
-  const int nb = (g.N + (PAIR ? 127 : 255)) / (PAIR ? 128 : 256), pairs = (g.K + 511) / 512;
-  const int chunks = g.chunks != nullptr ? *g.chunk_count : (g.P + TILE_ROWS - 1) / TILE_ROWS;
-  const int logical = xcd_logical(chunks * nb * splits);
-  if (logical < 0) return;
-  const int split = logical / (chunks * nb), item = logical - split * chunks * nb;
+  constexpr int COLS = PAIR ? TILE_COLS / 2 : TILE_COLS;
+  const int nb = (g.N + COLS - 1) / COLS, pairs = (g.K + 511) / 512, stages = (g.K + 255) / 256;
+  int nblk, first = 0, count = stages;
   Chunk c;
-  int nblk;
+  float *part = nullptr;
   if (g.chunks != nullptr) {
-    const int ci = item / nb;
-    nblk = item - ci * nb;
+    const int logical = xcd_logical(*g.chunk_count * nb);
+    if (logical < 0) return;
+    const int ci = logical / nb;
+    nblk = logical - ci * nb;
     const int4 v = g.chunks[ci];
     c = Chunk{v.x, v.y, v.z};
     if (c.n <= 0) return;  // rounding to whole tiles left it none
   } else {
+    const int big = cut * ((g.P + TILE_ROWS - 1) / TILE_ROWS), big8 = (big + 7) & ~7;
+    const bool is_big = (int)blockIdx.x < big8;
+    const int each = is_big ? TILE_ROWS : rows, cols = is_big ? cut : nb - cut, chunks = (g.P + each - 1) / each;
+    const int parts = is_big ? 1 : splits;
+    const int logical = tile_of(is_big ? blockIdx.x : blockIdx.x - big8, chunks * cols * parts);
+    if (logical < 0) return;
+    const int split = logical / (chunks * cols), item = logical - split * chunks * cols;
     // a few column tiles next to each other, then the next rows: what an XCD works
     // on at a time is near square
-    const int per = 4 * chunks, grp = item / per, in = item - grp * per, gn = min(4, nb - 4 * grp);
-    nblk = 4 * grp + in % gn;
+    const int per = 4 * chunks, grp = item / per, in = item - grp * per, gn = min(4, cols - 4 * grp);
+    nblk = (is_big ? 0 : cut) + 4 * grp + in % gn;
     const int ci = in / gn;
-    c = Chunk{0, TILE_ROWS * ci, min(TILE_ROWS, g.P - TILE_ROWS * ci)};
+    c = Chunk{0, each * ci, min(each, g.P - each * ci)};
+    if (parts > 1) {
+      first = 2 * (int)((long long)split * pairs / parts);
+      count = min(stages, 2 * (int)((long long)(split + 1) * pairs / parts)) - first;
+      part = partial + (long long)split * g.P * ((g.N + 3) & ~3);
+    }
   }
-  const int n0 = nblk * (PAIR ? 128 : 256);
-  const int stages = (g.K + 255) / 256;
-  const int first = 2 * (int)((long long)split * pairs / splits);
-  const int last = min(stages, 2 * (int)((long long)(split + 1) * pairs / splits));
-  float *part = splits > 1 ? partial + (long long)split * g.P * ((g.N + 3) & ~3) : nullptr;
+  const int n0 = nblk * COLS;
   switch ((c.n + 63) / 64) {
-    case 1: mx4_tile<1, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
-    case 2: mx4_tile<2, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
-    case 3: mx4_tile<3, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
-    default: mx4_tile<4, PAIR, SG>(g, c, n0, first, last - first, part, lds); break;
+    case 1: mx4_tile<1, PAIR, SG>(g, c, n0, first, count, part, lds); break;
+    case 2: mx4_tile<2, PAIR, SG>(g, c, n0, first, count, part, lds); break;
+    case 3: mx4_tile<3, PAIR, SG>(g, c, n0, first, count, part, lds); break;
+    default: mx4_tile<4, PAIR, SG>(g, c, n0, first, count, part, lds); break;
   }
 }
 
@@ -1087,22 +1132,17 @@ hipError_t launch_dequantize4(const uint8_t *q, long long ldq, const uint8_t *qs
 }
 
 namespace {
-void launch_tiles(const Mx4Args &g, long long items, int splits, float *partial, hipStream_t st) {
-  const dim3 gr((unsigned)((items * splits + 7) / 8 * 8)), blk(512);
+void launch_tiles(const Mx4Args &g, long long groups, int rows, int cut, int splits, float *partial, hipStream_t st) {
+  const dim3 gr((unsigned)groups), blk(512);
   if (scales_in_groups(g)) {
-    if (g.w[1] != nullptr) hipLaunchKernelGGL((mx4_tile_kernel<true, true>), gr, blk, 0, st, g, splits, partial);
-    else hipLaunchKernelGGL((mx4_tile_kernel<false, true>), gr, blk, 0, st, g, splits, partial);
+    if (g.w[1] != nullptr) hipLaunchKernelGGL((mx4_tile_kernel<true, true>), gr, blk, 0, st, g, rows, cut, splits, partial);
+    else hipLaunchKernelGGL((mx4_tile_kernel<false, true>), gr, blk, 0, st, g, rows, cut, splits, partial);
   } else {
-    if (g.w[1] != nullptr) hipLaunchKernelGGL((mx4_tile_kernel<true, false>), gr, blk, 0, st, g, splits, partial);
-    else hipLaunchKernelGGL((mx4_tile_kernel<false, false>), gr, blk, 0, st, g, splits, partial);
+    if (g.w[1] != nullptr) hipLaunchKernelGGL((mx4_tile_kernel<true, false>), gr, blk, 0, st, g, rows, cut, splits, partial);
+    else hipLaunchKernelGGL((mx4_tile_kernel<false, false>), gr, blk, 0, st, g, rows, cut, splits, partial);
   }
 }
-// parts of K where the tiles are fewer than the CUs, of four stages at least
-int dense_splits(int T, int N, int K) {
-  const long long tiles = (long long)((T + 255) / 256) * ((N + 255) / 256), pairs = (K + 511) / 512;
-  return (int)std::max(1LL, std::min({256 / tiles, pairs, 16LL}));
-}
-bool dense_streams(int T) { return T <= 64; }
+long long up8(long long v) { return (v + 7) / 8 * 8; }
 
 // an expert's rows up to which its weights are streamed by waves of their own
 constexpr int FEW_ROWS_4 = 32;
@@ -1115,28 +1155,27 @@ int stream_groups(const Mx4Args &g) {
 }
 }  // namespace
 
-size_t mx4_workspace_bytes(int T, int N, int K) {
-  if (dense_streams(T)) return 0;
-  const int s = dense_splits(T, N, K);
-  return s > 1 ? (size_t)s * T * ((N + 3) / 4) * 16 : 0;
-}
+size_t mx4_workspace_bytes(int T, int N, int K) { return mx4_partial_bytes(T, N, K); }
 
 hipError_t launch_mx4_gemm(const Mx4Args &g, void *ws, hipStream_t st) {
-  if (dense_streams(g.P)) {
+  const Mx4Plan p = mx4_plan(g.P, g.N, g.K);
+  if (p.stream) {
     const int nb = (g.N + 31) / 32;
     if (g.P <= 16) launch_stream<1, false, 8>(g, nb, st);
     else if (g.P <= 32) launch_stream<2, false, 8>(g, nb, st);
-    else launch_stream<4, false, 8>(g, nb, st);
+    else launch_stream<4, false, 8>(g, (long long)nb * ((g.P + 63) / 64), st);
     return hipGetLastError();
   }
-  const int splits = dense_splits(g.P, g.N, g.K);
-  launch_tiles(g, (long long)((g.P + 255) / 256) * ((g.N + 255) / 256), splits, static_cast<float *>(ws), st);
-  if (splits > 1) {
+  const int nb = (g.N + TILE_COLS - 1) / TILE_COLS;
+  const long long big = (long long)p.cut * ((g.P + TILE_ROWS - 1) / TILE_ROWS);
+  const long long rest = (long long)(nb - p.cut) * ((g.P + p.rows - 1) / p.rows) * p.splits;
+  launch_tiles(g, up8(big) + up8(rest), p.rows, p.cut, p.splits, static_cast<float *>(ws), st);
+  if (p.splits > 1) {
     const dim3 jr((unsigned)(((long long)g.P * ((g.N + 3) / 4) + 255) / 256));
     if (g.out_kind == MX4_OUT_BF16)
-      hipLaunchKernelGGL(mx4_join_kernel<MX4_OUT_BF16>, jr, dim3(256), 0, st, g, splits, static_cast<const float *>(ws));
+      hipLaunchKernelGGL(mx4_join_kernel<MX4_OUT_BF16>, jr, dim3(256), 0, st, g, p.splits, static_cast<const float *>(ws));
     else
-      hipLaunchKernelGGL(mx4_join_kernel<MX4_OUT_F32>, jr, dim3(256), 0, st, g, splits, static_cast<const float *>(ws));
+      hipLaunchKernelGGL(mx4_join_kernel<MX4_OUT_F32>, jr, dim3(256), 0, st, g, p.splits, static_cast<const float *>(ws));
   }
   return hipGetLastError();
 }
@@ -1165,7 +1204,7 @@ hipError_t launch_mx4_expert(const Mx4Args &a, void *ws, hipStream_t st) {
   if (many_chunks(E, g.P) > 0) {
     g.chunks = many;
     g.chunk_count = count + 1;
-    launch_tiles(g, (long long)many_chunks(E, g.P) * ((g.N + (pair ? 127 : 255)) / (pair ? 128 : 256)), 1, nullptr, st);
+    launch_tiles(g, up8((long long)many_chunks(E, g.P) * ((g.N + (pair ? 127 : 255)) / (pair ? 128 : 256))), 0, 0, 1, nullptr, st);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   g.chunks = few;

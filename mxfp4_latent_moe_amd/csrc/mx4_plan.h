@@ -1,0 +1,81 @@
+// Which kernel of the dense MXFP4 product runs, and how it is cut: host code
+// alone, a function of the sizes.
+#pragma once
+#include <stddef.h>
+
+#include <algorithm>
+
+namespace moe {
+
+// How a product of T rows and N columns over K is cut, and what it then takes, in us.
+//
+// Stream: work-groups of 32 columns and up to 64 rows, whose eight waves take the
+// stages of 256 inputs in turn; one on a CU at a time.
+// Tiles: work-groups of 256 columns and `rows` rows (64 to 256).  With more of them
+// than CUs (256) the first `cut` column tiles may have 256 rows, which read least for
+// a product, and the others fewer, which fill the last round better.  Where tiles are
+// fewer than the CUs K may be split, and the parts' sums are joined.
+//
+// Measured, bf16 out, K = 7168 unless said, us: stream / tiles of 64 rows / of 128 /
+// of 256 (K split so that all CUs have a part), and what this rule takes:
+// (tokens, columns) (32, 3584) 8.9 / 14.9 / - / -, stream; (64, 3584) 13.4 / 17.4,
+// stream; (64, 7168, K 33792) 61 / 38, tiles; (128, 3584) 14.6 / 17.8 / 21.5, stream;
+// (301, 895) 14.1 / 16.9 / 19.7 / 22.2, stream; (512, 3584) 51 / 21.9 / 24.1 / 34,
+// tiles of 64; (1024, 3584) 87 / 25.2 / 31.1 / 38.7; (2048, 3584) 166 / 51 / 38.7 /
+// 52.7, tiles of 128; (4096, 4096) - / 108 / 80 / 68, tiles of 256; (4096, 6144)
+// - / 151 / 114 / 110, one round of 256 rows and one of 128: 105.
+struct Mx4Plan {
+  bool stream;
+  int rows, cut, splits;
+  double us;
+};
+
+constexpr long long MX4_CUS = 256;
+inline long long mx4_up(long long a, long long b) { return (a + b - 1) / b; }
+
+inline double mx4_stream_us(int T, int N, int K) {
+  const long long stages = mx4_up(K, 256), groups = mx4_up(N, 32) * mx4_up(T, 64);
+  const double stage = T <= 16 ? 1.7 : T <= 32 ? 2.4 : 3.3;  // of eight waves
+  return 1.0 + stage * (double)(mx4_up(groups, MX4_CUS) * mx4_up(stages, 8));
+}
+// the ends of a kernel of such tiles, and a stage of them on every CU
+inline double mx4_ends_us(int rows) { return rows <= 64 ? 4.5 : rows <= 128 ? 5.0 : rows <= 192 ? 6.0 : 7.5; }
+inline double mx4_stage_us(int rows) { return rows <= 64 ? 0.75 : rows <= 128 ? 1.1 : rows <= 192 ? 1.45 : 1.85; }
+
+inline Mx4Plan mx4_plan(int T, int N, int K) {
+  const long long stages = mx4_up(K, 256), pairs = mx4_up(K, 512), nb = mx4_up(N, 256);
+  Mx4Plan best{true, 0, 0, 1, mx4_stream_us(T, N, K)};
+  if (T <= 16) return best;  // a tile would be three quarters empty
+  const double out = 0.4e-6 * T * N;                               // rows written
+  const double in = ((double)N + T) * K * (17.0 / 32.0) / 5.3e6;  // operands read once
+  for (int rows = 64; rows <= 256; rows += 64) {
+    const long long tiles = mx4_up(T, rows) * nb;
+    for (long long s = 1; s <= std::min(pairs, 16LL) && (s == 1 || tiles * s <= MX4_CUS); ++s) {
+      const long long per = s > 1 ? 2 * mx4_up(pairs, s) : stages;
+      const double join = s > 1 ? 6.0 + 0.3 * (double)s + 0.5e-6 * (double)s * T * N : 0.0;
+      const double run = mx4_stage_us(rows) * (double)(mx4_up(tiles * s, MX4_CUS) * per);
+      const double us = mx4_ends_us(rows) + out + join + std::max(run, in);
+      if (us < best.us) best = {false, rows, 0, (int)s, us};
+    }
+    // whole rounds of the largest tiles first
+    const long long tt = mx4_up(T, 256);
+    for (long long rounds = 1; rows < 256 && rounds <= 64; ++rounds) {
+      const long long cut = rounds * MX4_CUS / tt;
+      if (cut >= nb) break;
+      if (cut == 0) continue;
+      const double run = (double)stages * (mx4_stage_us(256) * (double)mx4_up(cut * tt, MX4_CUS) +
+                                           mx4_stage_us(rows) * (double)mx4_up((nb - cut) * mx4_up(T, rows), MX4_CUS));
+      const double us = mx4_ends_us(256) + out + std::max(run, in);
+      if (us < best.us) best = {false, rows, (int)cut, 1, us};
+    }
+  }
+  return best;
+}
+
+// bytes of the parts' sums
+inline size_t mx4_partial_bytes(int T, int N, int K) {
+  const Mx4Plan p = mx4_plan(T, N, K);
+  return !p.stream && p.splits > 1 ? (size_t)p.splits * T * ((N + 3) / 4) * 16 : 0;
+}
+
+}  // namespace moe

@@ -65,7 +65,8 @@ def test_gemm(lib):
     for T, N, K in ((-1, 1, 32), (1, 0, 32), (1, 1, 0), (1, 1, 48), (1, 1, 1 << 21)):
         assert lib.moe_mxfp4_gemm_workspace_bytes(T, N, K) == 0
     assert lib.moe_mxfp4_gemm_workspace_bytes(0, 1, 32) > 0
-    assert lib.moe_mxfp4_gemm_workspace_bytes(1 << 21, 1 << 20, 1 << 20) > 0
+    assert lib.moe_mxfp4_gemm_workspace_bytes(1 << 21, 1 << 12, 1 << 20) > 0
+    assert lib.moe_mxfp4_gemm_workspace_bytes(1 << 21, (1 << 12) + 1, 1 << 20) == 0
 
 
 def test_expert_gemm(lib):
@@ -93,14 +94,15 @@ def test_expert_gemm(lib):
                 dict(**down, **four), {**four, "out_scale": None}, {**four, "ldo": 24}, {**four, "ldo": 40},
                 {**four, "ldos": 1}, {**four, "out": FAKE + 8}):
         assert call(**bad) == EINVAL, bad
-    for bad in (dict(n_experts=1025), dict(K=144), dict(P=(1 << 21) + 1), dict(N=(1 << 20) + 1, ldo=1 << 21),
-                dict(ldx=(1 << 22) + 16), dict(ldxs=(1 << 22) + 1), dict(x_rows=1 << 30),
+    for bad in (dict(n_experts=1025), dict(K=144), dict(P=(1 << 21) + 1), dict(N=(1 << 18) + 1, ldo=1 << 21),
+                dict(ldx=(1 << 22) + 16), dict(ldxs=(1 << 22) + 1), dict(x_rows=1 << 30), dict(P=1 << 20, N=1 << 14, ldo=1 << 14),
                 dict(x_rows=1 << 21, ldx=1 << 10), {**four, "N": 72, "ldo": 48, "ldos": 3}):
         assert call(**bad) == ENOTSUP, bad
     assert call(wsb=ws - 1) == EWS and call(**down, wsb=ws - 1) == EWS and call(**four, wsb=ws - 1) == EWS
     for E, P, N, K in ((0, 1, 1, 32), (1025, 1, 1, 32), (1, -1, 1, 32), (1, 1, 0, 32), (1, 1, 1, 40), (1, 1 << 22, 1, 32)):
         assert lib.moe_mxfp4_expert_gemm_workspace_bytes(E, P, N, K) == 0
-    assert lib.moe_mxfp4_expert_gemm_workspace_bytes(1024, 1 << 21, 1 << 20, 1 << 20) > 0
+    assert lib.moe_mxfp4_expert_gemm_workspace_bytes(1024, 1 << 15, 1 << 18, 1 << 20) > 0
+    assert lib.moe_mxfp4_expert_gemm_workspace_bytes(1024, 1 << 21, 1 << 12, 1 << 20) > 0
 
 
 def test_struct_layout(tmp_path):

@@ -237,6 +237,25 @@ def test_full_sizes(mx, T):
     assert (f64(out)[ts] == ref).all()
 
 
+# whole tiles of every height, a round of the largest with lower ones behind it, K in parts: test_mx4_plan_host.py
+# holds the plan to that
+LARGE = [(301, 895, 7168), (512, 3584, 7168), (1500, 2100, 256), (2900, 4400, 1056), (4100, 6200, 768),
+         (3000, 6600, 1536), (4096, 4096, 4096)]
+
+
+@pytest.mark.parametrize("T,N,K", LARGE)
+def test_tiles(mx, T, N, K):
+    """Every result, against the same product in float64 on the GPU (exact there as here)."""
+    for out_kind, opad in (("f32", 0), ("bf16", 8), ("bf16", 4), ("bf16", 1)):
+        say(f"case: 4-bit product by tiles T={T} N={N} K={K} out {out_kind} pad {opad}")
+        x, xs, [(w, ws)] = operands(np.random.default_rng(T), T, N, K)
+        out = torch.full((T, N + opad), 3.0, dtype=DT[out_kind], device=DEV)
+        scratch = torch.full((mx.mxfp4_gemm_workspace_bytes(T, N, K),), 0xFF, dtype=torch.uint8, device=DEV)
+        mx.mxfp4_gemm(dev(x), dev(xs)[:, :K // 32], dev(w[0]), dev(ws[0]), out[:, :N], scratch)
+        a, b = dev(mx4.dequantize(x, xs[:, :K // 32], K)), dev(mx4.dequantize(w[0], ws[0], K).T)
+        assert torch.equal(out[:, :N], (a @ b).to(DT[out_kind])) and (out[:, N:] == 3.0).all()
+
+
 # ---- expert products
 
 def routing(rng, counts, tokens, top_k, spare):

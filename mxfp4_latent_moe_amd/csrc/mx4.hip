@@ -1144,8 +1144,10 @@ void launch_tiles(const Mx4Args &g, long long groups, int rows, int cut, int spl
 }
 long long up8(long long v) { return (v + 7) / 8 * 8; }
 
-// an expert's rows up to which its weights are streamed by waves of their own
-constexpr int FEW_ROWS_4 = 32;
+// An expert's rows up to which its weights are streamed by waves of their own.  The down product of 256
+// tokens over 64 experts, four each, uneven: 61 us at 16, 61 at 8, 68 at 24, 69 at 32; gate and up of 64
+// tokens 94, 91, 101, 105; of 1024 tokens, two each, 168, 169, 188, 184.
+constexpr int FEW_ROWS_4 = 16;
 int few_chunks(int E, int P) { return std::min(E, P); }
 int many_chunks(int E, int P) { return P / TILE_ROWS + std::min(E, P / (FEW_ROWS_4 + 1)); }
 // work-groups of the stream kernel for a chunk
@@ -1209,8 +1211,8 @@ hipError_t launch_mx4_expert(const Mx4Args &a, void *ws, hipStream_t st) {
   }
   g.chunks = few;
   g.chunk_count = count;
-  if (pair) launch_stream<2, true, 1>(g, (long long)few_chunks(E, g.P) * groups, st);
-  else launch_stream<2, false, 1>(g, (long long)few_chunks(E, g.P) * groups, st);
+  if (pair) launch_stream<1, true, 1>(g, (long long)few_chunks(E, g.P) * groups, st);
+  else launch_stream<1, false, 1>(g, (long long)few_chunks(E, g.P) * groups, st);
   return hipGetLastError();
 }
 

@@ -157,8 +157,9 @@ struct Chunk {
 
 // The experts' sorted rows as chunks, an expert's one after the other: experts of
 // up to `few` rows on the list few_list, one chunk each, the others on many_list in
-// chunks of at most `most` rows, in whole tiles of 64 of one size.  Bad offsets give
-// wrong chunks but none outside the P rows and the lists' sizes.
+// chunks of at most `most` rows, blocks of 64 shared evenly, with a chunk's number
+// within its expert << 16 | how many those are.  Bad offsets give wrong
+// chunks but none outside the P rows and the lists' sizes.
 __global__ __launch_bounds__(1024) void mx4_plan_kernel(const int32_t *offsets, int E, int P, int few, int most,
                                                         int few_cap, int4 *few_list, int32_t *few_count, int many_cap,
                                                         int4 *many_list, int32_t *many_count) {
@@ -189,10 +190,12 @@ __global__ __launch_bounds__(1024) void mx4_plan_kernel(const int32_t *offsets, 
       sum[l] += tot[l][w];
     }
   if (n[0] && at[0] < few_cap) few_list[at[0]] = int4{e, lo, ne, 0};
-  const int each = n[1] > 0 ? ((ne + n[1] - 1) / n[1] + 63) / 64 * 64 : 0;
-  for (int i = 0; i < n[1] && at[1] + i < many_cap; ++i)
-    if (i * each < ne) many_list[at[1] + i] = int4{e, lo + i * each, min(each, ne - i * each), 0};
-    else many_list[at[1] + i] = int4{e, lo, 0, 0};
+  const int listed = min(n[1], many_cap - at[1]);
+  const long long blocks = (ne + 63) / 64;  // of 64 rows
+  for (int i = 0; i < listed; ++i) {
+    const int from = 64 * (int)(blocks * i / n[1]), to = min(64 * (int)(blocks * (i + 1) / n[1]), ne);
+    many_list[at[1] + i] = int4{e, lo + from, to - from, i << 16 | listed};
+  }
   if (e == 0) {
     *few_count = min(sum[0], few_cap);
     *many_count = min(sum[1], many_cap);
@@ -1014,6 +1017,14 @@ MOE_DEV int tile_of(int block, int total) {
   return block < t8 && id < total ? id : -1;
 }
 
+// chunk and column tile of item i of chunks * cols: four column tiles next to each
+// other, then the next chunk, so that what an XCD works on at a time is near square
+MOE_DEV void tile_at(int i, int chunks, int cols, int &chunk, int &col) {
+  const int per = 4 * chunks, grp = i / per, in = i - grp * per, gn = min(4, cols - 4 * grp);
+  chunk = in / gn;
+  col = 4 * grp + in - chunk * gn;
+}
+
 // grouped: an item is a chunk and a tile of columns.  Dense: tiles of 256 rows for
 // the first `cut` column tiles, of `rows` for the others, whose K may be split
 template <bool PAIR, bool SG>
@@ -1021,17 +1032,16 @@ __global__ __launch_bounds__(512, 2) void mx4_tile_kernel(Mx4Args g, int rows, i
   __shared__ __attribute__((aligned(1024))) uint8_t lds[TILE_LDS];
   constexpr int COLS = PAIR ? TILE_COLS / 2 : TILE_COLS;
   const int nb = (g.N + COLS - 1) / COLS, pairs = (g.K + 511) / 512, stages = (g.K + 255) / 256;
-  int nblk, first = 0, count = stages;
+  int nblk, cj, first = 0, count = stages;
   Chunk c;
   float *part = nullptr;
   if (g.chunks != nullptr) {
     const int logical = xcd_logical(*g.chunk_count * nb);
     if (logical < 0) return;
-    const int ci = logical / nb;
-    nblk = logical - ci * nb;
-    const int4 v = g.chunks[ci];
+    const int ci = logical / nb, info = g.chunks[ci].w, c0 = ci - (info >> 16);  // the expert's first
+    tile_at(logical - c0 * nb, info & 0xFFFF, nb, cj, nblk);
+    const int4 v = g.chunks[c0 + cj];
     c = Chunk{v.x, v.y, v.z};
-    if (c.n <= 0) return;  // rounding to whole tiles left it none
   } else {
     const int big = cut * ((g.P + TILE_ROWS - 1) / TILE_ROWS), big8 = (big + 7) & ~7;
     const bool is_big = (int)blockIdx.x < big8;
@@ -1040,12 +1050,9 @@ __global__ __launch_bounds__(512, 2) void mx4_tile_kernel(Mx4Args g, int rows, i
     const int logical = tile_of(is_big ? blockIdx.x : blockIdx.x - big8, chunks * cols * parts);
     if (logical < 0) return;
     const int split = logical / (chunks * cols), item = logical - split * chunks * cols;
-    // a few column tiles next to each other, then the next rows: what an XCD works
-    // on at a time is near square
-    const int per = 4 * chunks, grp = item / per, in = item - grp * per, gn = min(4, cols - 4 * grp);
-    nblk = (is_big ? 0 : cut) + 4 * grp + in % gn;
-    const int ci = in / gn;
-    c = Chunk{0, each * ci, min(each, g.P - each * ci)};
+    tile_at(item, chunks, cols, cj, nblk);
+    if (!is_big) nblk += cut;
+    c = Chunk{0, each * cj, min(each, g.P - each * cj)};
     if (parts > 1) {
       first = 2 * (int)((long long)split * pairs / parts);
       count = min(stages, 2 * (int)((long long)(split + 1) * pairs / parts)) - first;

@@ -150,6 +150,32 @@ MOE_DEV f32x4_t mfma_4_16(u32x4_t w, u32x4_t x, f32x4_t c, uint32_t sw, uint32_t
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, J, (int)sw, J, (int)sx);
 }
 
+// tanh x as a fraction: x P(x^2) over Q(x^2), both of degree 4 with positive
+// coefficients, fitted for the least relative error over |x| <= 9 (2.1e-8; in fp32
+// 3.0e-7), past which tanh is within 3.1e-8 of its limit.  NaN stays NaN.
+MOE_DEV void tanh_ratio(float x, float &num, float &den) {
+  const float c = __builtin_elementwise_minimum(__builtin_elementwise_maximum(x, -9.0f), 9.0f), t = c * c;
+  float p = 2.6083236265e-11f, q = 1.5188552638e-9f;
+  p = fmaf(p, t, 4.0252043476e-8f);
+  q = fmaf(q, t, 6.4172485281e-7f);
+  p = fmaf(p, t, 6.8273161560e-6f);
+  q = fmaf(q, t, 5.0540962548e-5f);
+  p = fmaf(p, t, 2.6134811924e-4f);
+  q = fmaf(q, t, 9.1238942696e-4f);
+  num = c * fmaf(p, t, 0.001953125f);
+  den = fmaf(q, t, 0.001953125f);
+}
+
+// SiTU-GLU of a tile's sums: 31 instructions a value where situ_glu has 43.  Denominators lie
+// between 2^-9 and 1, so that their product overflows where 1 + exp(-g) does (there the result is 0).
+MOE_DEV float situ4(float g, float u, float beta, float beta_lin) {
+  float ng, dg, nu, du;
+  tanh_ratio(g * __builtin_amdgcn_rcpf(beta), ng, dg);
+  tanh_ratio(u * __builtin_amdgcn_rcpf(beta_lin), nu, du);
+  const float ds = 1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f);
+  return (ng * __builtin_amdgcn_rcpf(dg * du * ds)) * (nu * (beta * beta_lin));
+}
+
 // an expert's rows [row, row + n) of a grouped product, or rows of the dense one
 struct Chunk {
   int expert, row, n;
@@ -573,7 +599,7 @@ MOE_DEV void mx4_stream(const Mx4Args &g, const Chunk &c, int block, uint8_t *ld
     if constexpr (PAIR) {
       f32x4_t v;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = situ_glu(acc[0][i][k], acc[1][i][k], g.beta, g.beta_lin);
+      for (int k = 0; k < 4; ++k) v[k] = situ4(acc[0][i][k], acc[1][i][k], g.beta, g.beta_lin);
       const int n = n0 + 4 * kg;
       if (g.out_kind == MX4_OUT_MX4) {
         // a block of the result is this wave's columns and its neighbour's
@@ -931,7 +957,7 @@ MOE_DEV void mx4_tile(const Mx4Args &g, const Chunk &c, int n0, int first, int c
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if constexpr (PAIR) v[q][k] = situ_glu(acc[0][i][4 * q + k], acc[1][i][4 * q + k], g.beta, g.beta_lin);
+          if constexpr (PAIR) v[q][k] = situ4(acc[0][i][4 * q + k], acc[1][i][4 * q + k], g.beta, g.beta_lin);
           else v[q][k] = acc[m][i][4 * q + k];
         }
       if (PAIR && g.out_kind == MX4_OUT_MX4) {

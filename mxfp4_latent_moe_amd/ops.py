@@ -448,11 +448,18 @@ class LatentMoE:
     hi + lo planes (buffer "H", int16 bits [T k, 2 I]) and the down call
     reads them, with no split pass in between; Y and the output are bitwise
     those of the fp32 H.  h_planes=False keeps H in fp32 always.
+
+    mxfp4_rows: the routed experts' products with both operands in MXFP4:
+    mxfp4_quantize of z (buffers "zq", "zq_scale"), mxfp4_expert_gemm (gate/up +
+    SiTU-GLU) with H in MXFP4 too ("H", codes, and "H_scale"), and
+    mxfp4_expert_gemm (down) to Y.  Activations then keep four bits of each
+    value where operand modes keep 8 to 24, in exchange for the 4-bit matrix
+    rate.  Single bank, latent and inter multiples of 32; off by default.
     """
 
     def __init__(self, shape: MoeShape, weights: dict, device="cuda", overlap_shared: bool = True,
                  latent_on_side: bool = True, late_shared_join: bool = True, bank_b: dict | None = None,
-                 h_planes: bool = True):
+                 h_planes: bool = True, mxfp4_rows: bool = False):
         missing = [k for k in WEIGHT_KEYS if k not in weights]
         if missing:
             raise ValueError(f"missing weights: {missing}")
@@ -462,6 +469,9 @@ class LatentMoE:
         # MXFP4) and bank_b = {"format": MOE_WF_*, "n_experts": n_b, tensors...}
         # holds the rest; the expert GEMMs then run moe_grouped_gemm_two_bank
         self.bank_b = bank_b
+        if mxfp4_rows and (bank_b is not None or shape.latent % 32 or shape.inter % 32):
+            raise ValueError("mxfp4_rows: want one bank of experts, latent and inter multiples of 32")
+        self.mxfp4_rows = mxfp4_rows
         if bank_b is not None:
             n_b = int(bank_b["n_experts"])
             n_a = shape.n_experts - n_b
@@ -493,7 +503,7 @@ class LatentMoE:
     def planes_for(self, T: int) -> bool:
         """Whether H travels as bf16 planes at T tokens (see h_planes)."""
         s = self.shape
-        return (self.h_planes and self.bank_b is None and s.operand_mode in (_lib.MOE_OPND_BF16X2, _lib.MOE_OPND_BF16)
+        return (self.h_planes and self.bank_b is None and not self.mxfp4_rows and s.operand_mode in (_lib.MOE_OPND_BF16X2, _lib.MOE_OPND_BF16)
                 and T * s.top_k >= 8 * s.n_experts)
 
     def buffers(self, T: int) -> dict:
@@ -504,6 +514,9 @@ class LatentMoE:
         gfn = _lib.MOE_FN_GROUPED_GEMM_TWO_BANK if self.bank_b is not None else MOE_FN_GROUPED_GEMM
         ws = max(workspace_bytes(s, fn, P if fn == gfn else T)
                  for fn in (MOE_FN_ROUTE, MOE_FN_PERMUTE, gfn, MOE_FN_COMBINE_NORM_UP))
+        if self.mxfp4_rows:
+            ws = max(ws, *(mxfp4_expert_gemm_workspace_bytes(s.n_experts, P, n, k)
+                           for n, k in ((s.inter, s.latent), (s.latent, s.inter))))
         ws_sh = max(16, workspace_bytes(s, MOE_FN_SHARED_FFN, T), workspace_bytes(s, MOE_FN_ROUTE, T))
         i32, f32 = torch.int32, torch.float32
         b = {
@@ -516,12 +529,16 @@ class LatentMoE:
             "pair_pos": torch.empty((P,), dtype=i32, device=dev),
             "active": torch.empty((s.n_experts + 1,), dtype=i32, device=dev),
             "H": (torch.empty((P, 2 * s.inter), dtype=torch.int16, device=dev) if self.planes_for(T)
-                  else torch.empty((P, s.inter), dtype=f32, device=dev)),
+                  else None if self.mxfp4_rows else torch.empty((P, s.inter), dtype=f32, device=dev)),
             "Y": torch.empty((P, s.latent), dtype=f32, device=dev),
             "out": torch.empty((T, s.hidden), dtype=f32, device=dev),
             "ws": torch.empty((ws,), dtype=torch.uint8, device=dev),
             "ws_shared": torch.empty((ws_sh,), dtype=torch.uint8, device=dev),
         }
+        if self.mxfp4_rows:
+            for name, rows, n in (("zq", T, s.latent), ("H", P, s.inter)):
+                b[name] = torch.empty((rows, n // 2), dtype=torch.uint8, device=dev)
+                b[name + "_scale"] = torch.empty((rows, n // 32), dtype=torch.uint8, device=dev)
         self._bufs[T] = b
         self._streams["forward", T] = {torch.cuda.current_stream(dev).cuda_stream}
         return b
@@ -598,6 +615,16 @@ class LatentMoE:
             call("grouped_gemm_down", st,
                  lambda: grouped_gemm_two_bank(s, MOE_OP_DOWN, P, b["offsets"], b["sorted_pair"], b["H"], da, db,
                                                None, b["Y"], ws, st))
+        elif self.mxfp4_rows:
+            call("mxfp4_quantize_z", st, lambda: mxfp4_quantize(b["z"], b["zq"], b["zq_scale"], stream=st))
+            call("grouped_gemm_gateup", st,
+                 lambda: mxfp4_expert_gemm(b["zq"], b["zq_scale"], w["w1_packed"], w["w1_scale"], b["offsets"], b["H"], ws,
+                                           w3=w["w3_packed"], w3_scale=w["w3_scale"], sorted_pair=b["sorted_pair"],
+                                           top_k=s.top_k, beta=s.beta, beta_lin=s.beta_lin, out_scale=b["H_scale"],
+                                           stream=st))
+            call("grouped_gemm_down", st,
+                 lambda: mxfp4_expert_gemm(b["H"], b["H_scale"], w["w2_packed"], w["w2_scale"], b["offsets"], b["Y"], ws,
+                                           stream=st))
         else:
             planes = self.planes_for(T)
             call("grouped_gemm_gateup", st,
@@ -644,6 +671,8 @@ class LatentMoE:
         take activations at fp32 precision whatever operand_mode is.  A two-bank layer has no such form."""
         if self.bank_b is not None:
             raise ValueError("forward_few: the two-bank layer has no few-token form")
+        if self.mxfp4_rows:
+            raise ValueError("forward_few: its products take activations at fp32 precision, not as MXFP4 rows")
         T = x.shape[0]
         if x.dim() != 2 or not 1 <= T <= _lib.MOE_FEW_MAX_T or x.shape[1] != self.shape.hidden:
             raise ValueError(f"forward_few: x is {tuple(x.shape)}, want [1..{_lib.MOE_FEW_MAX_T}, {self.shape.hidden}]")

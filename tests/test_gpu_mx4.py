@@ -394,6 +394,32 @@ def test_expert_full_sizes(mx, counts):
     assert (np.abs(f64(y)[ps] - ref) <= (128 + I // 64 + 16) * 2.0 ** -23 * mag).all()
 
 
+@pytest.mark.parametrize("rows,N", [(3, 64), (70, 64), (300, 16384)])
+def test_expert_glu_not_finite(mx, rows, N):
+    """Products that are infinite or NaN, by waves that stream and by tiles: SiTU-GLU's limits."""
+    say(f"case: SiTU-GLU of infinite products, {rows} rows, {N} columns")
+    K, T = 32, rows
+    x, xs = np.full((T, K // 2), 0x22, np.uint8), np.full((T, 1), 127, np.uint8)  # ones
+    # value and scale byte of a row's codes: 32 * 6 * 2^127 and NaN, else 16 and 2
+    kinds = {"inf": (0x77, 254), "-inf": (0xFF, 254), "nan": (0x22, 255), "16": (0x11, 127), "-2": (0x99, 124)}
+    pairs = [(a, b) for a in kinds for b in kinds]
+    at = np.arange(N) % len(pairs)
+    w = [np.stack([np.full(K // 2, kinds[pairs[i][m]][0], np.uint8) for i in at])[None] for m in range(2)]
+    s = [np.array([[kinds[pairs[i][m]][1]] for i in at], np.uint8)[None] for m in range(2)]
+    with np.errstate(invalid="ignore"):
+        value = [np.array([float(pairs[i][m]) for i in at]) for m in range(2)]
+        g, u = value
+        ref = 4 * np.tanh(g / 4) * 25 * np.tanh(u / 25) * np.where(g == -np.inf, 0, 1 / (1 + np.exp(-np.maximum(g, -700))))
+    out = torch.empty((T, N), device=DEV)
+    scratch = torch.empty(mx.mxfp4_expert_gemm_workspace_bytes(1, T, N, K), dtype=torch.uint8, device=DEV)
+    mx.mxfp4_expert_gemm(dev(x), dev(xs), dev(w[0]), dev(s[0]), dev(np.array([0, T], np.int32)), out, scratch,
+                         w3=dev(w[1]), w3_scale=dev(s[1]), sorted_pair=dev(np.arange(T, dtype=np.int32)), top_k=1)
+    got = f64(out)
+    assert (np.isnan(got) == np.isnan(ref)).all()
+    ok = ~np.isnan(ref)
+    assert (np.abs(got[:, ok] - ref[ok]) <= np.abs(ref[ok]) * (32 + 16) * 2.0 ** -23).all()
+
+
 def test_streams_and_replays(mx):
     """Two calls at once with a workspace each; two captured calls that share one, replayed in turn with eager work in
     between, every replay the eager result."""

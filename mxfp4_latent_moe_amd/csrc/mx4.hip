@@ -1180,9 +1180,13 @@ long long up8(long long v) { return (v + 7) / 8 * 8; }
 // An expert's rows up to which its weights are streamed by waves of their own.  The down product of 256
 // tokens over 64 experts, four each, uneven: 61 us at 16, 61 at 8, 68 at 24, 69 at 32; gate and up of 64
 // tokens 94, 91, 101, 105; of 1024 tokens, two each, 168, 169, 188, 184.
-constexpr int FEW_ROWS_4 = 16;
-int few_chunks(int E, int P) { return std::min(E, P); }
-int many_chunks(int E, int P) { return P / TILE_ROWS + std::min(E, P / (FEW_ROWS_4 + 1)); }
+// With 32 rows an expert on average and more, tiles take them all, as the few that the others would have are
+// not worth a launch behind them: of 4096 tokens, two of 112 experts each, gate and up 339 with both, 330 with
+// tiles alone, down 191 and 184; of 1024 tokens, two of 64 each, down 116 and 100 (with experts' weights e^1.5
+// apart, the rows with a few of them, 67 and 71).
+int few_rows(int E, int P) { return P >= 32LL * E ? 0 : 16; }
+int few_chunks(int E, int P) { return few_rows(E, P) > 0 ? std::min(E, P) : 0; }
+int many_chunks(int E, int P) { return P / TILE_ROWS + std::min(E, P / (few_rows(E, P) + 1)); }
 // work-groups of the stream kernel for a chunk
 int stream_groups(const Mx4Args &g) {
   const int cols = g.w[1] != nullptr ? 64 : 128;
@@ -1232,7 +1236,7 @@ hipError_t launch_mx4_expert(const Mx4Args &a, void *ws, hipStream_t st) {
   }
   int32_t *count = static_cast<int32_t *>(ws);
   int4 *few = reinterpret_cast<int4 *>(static_cast<char *>(ws) + 256), *many = few + few_chunks(E, g.P);
-  hipLaunchKernelGGL(mx4_plan_kernel, dim3(1), dim3(1024), 0, st, g.offsets, E, g.P, FEW_ROWS_4, TILE_ROWS,
+  hipLaunchKernelGGL(mx4_plan_kernel, dim3(1), dim3(1024), 0, st, g.offsets, E, g.P, few_rows(E, g.P), TILE_ROWS,
                      few_chunks(E, g.P), few, count, many_chunks(E, g.P), many, count + 1);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -1242,6 +1246,7 @@ hipError_t launch_mx4_expert(const Mx4Args &a, void *ws, hipStream_t st) {
     launch_tiles(g, up8((long long)many_chunks(E, g.P) * ((g.N + (pair ? 127 : 255)) / (pair ? 128 : 256))), 0, 0, 1, nullptr, st);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
+  if (few_chunks(E, g.P) == 0) return hipSuccess;
   g.chunks = few;
   g.chunk_count = count;
   if (pair) launch_stream<1, true, 1>(g, (long long)few_chunks(E, g.P) * groups, st);

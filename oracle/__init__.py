@@ -29,6 +29,7 @@ Modules:
              per-pair Python loops, its own bit-level e2m1 decoding)
   reap    -- REAP expert saliency over a calibration batch (README, REAP
              section)
+  mx4     -- values to MXFP4 rows and back, products of such rows by expert
   promotion -- the moe_k_hi cap on promoted (MXFP4) experts per token
              (Kimi-K3-Alis-MLX-Dynamic card, Build recipe)
 

@@ -347,6 +347,15 @@ def test_expert_odd_columns(mx):
         expert(mx, [5, 0, 70], 77, 160, True, out, tokens=9, top_k=2, opad=3)
 
 
+@pytest.mark.parametrize("counts", [[1, 400, 0, 17, 2, 300], [1] * 12 + [0, 200, 16, 65, 17, 3, 0, 129, 2, 33, 0, 1]])
+def test_expert_lists(mx, counts):
+    """Wide enough for lists of chunks: tiles alone, and both kernels."""
+    expert(mx, counts, 4160, 64, True, "mx4", tokens=50, top_k=3, seed=3)
+    expert(mx, counts, 4161, 64, True, "f32", tokens=50, top_k=3, seed=4, spare=5)
+    expert(mx, counts, 8323, 96, False, "bf16", seed=5, opad=5)
+    expert(mx, counts, 8320, 544, False, "f32", weights=True, seed=6, spare=70)
+
+
 def test_expert_many_experts(mx):
     rng = np.random.default_rng(8)
     counts = rng.permutation(np.concatenate([np.zeros(800, int), rng.integers(1, 5, 200), [70] * 24]))

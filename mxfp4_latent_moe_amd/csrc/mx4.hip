@@ -28,8 +28,9 @@ MOE_DEV uint32_t max4(uint32_t m) {
   return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));  // 2 3 0 1
 }
 
-// Rows of fp32 or bf16 values in MXFP4: a block is four lanes of 8 values.
-// vec: rows' chunks of 8 are whole and aligned.
+// Rows of fp32 or bf16 values in MXFP4: a block is four lanes of 8 values, read in
+// 16-byte loads, one pass.  vec: rows' chunks of 8 are whole and aligned.  Memory is
+// the bound: 16384 x 3584 fp32 50 us, 5.3 TB/s read and written; a row of 7168 2.4 us.
 template <typename X>
 __global__ __launch_bounds__(256) void quantize4_kernel(const X *__restrict__ x, long long ldx, long long T, int K,
                                                         int vec, int ocp, uint8_t *__restrict__ q, long long ldq,
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(256) void quantize4_kernel(const X *__restrict__ x,
   if ((threadIdx.x & 3) == 0) qs[t * ldqs + b] = (uint8_t)sb;
 }
 
-// and back, eight values a thread
+// and back, eight values a thread: 16384 x 3584 to bf16 24 us, 6.2 TB/s
 template <typename O>
 __global__ __launch_bounds__(256) void dequantize4_kernel(const uint8_t *__restrict__ q, long long ldq,
                                                           const uint8_t *__restrict__ qs, long long ldqs, long long T,
@@ -349,8 +350,13 @@ MOE_DEV bool find_chunk(const Mx4Args &g, int rows, int want, Chunk &c, int *lds
 //
 // Loads of two bytes a lane cost as much as those of sixteen.  With SG (scale rows
 // are whole dwords apart and aligned) the scales of two stages come into LDS by one
-// direct load for 32 rows, 16 bytes a row and stage; without it byte by byte to
-// registers.  7168 x 33792: one token 25 us, 16 tokens 31
+// direct load for 32 rows, 16 bytes a row; without it byte by byte to registers
+// (39 us in place of 31 at 16 tokens, 7168 x 33792).
+//
+// Bound by the weights.  One token: 3584 x 7168 5.9 us, 7168 x 33792 25 us, 5.1 TB/s;
+// 16 tokens 31 us, 4.2 TB/s, where half as many bytes of x as of weights come to a
+// CU.  Gate and up of one token's 16 experts 41 us, 4.5 TB/s; of 16 tokens through 896
+// experts (some 224 of them in use) 440 us, 5.9 TB/s, down 220 to 245.
 constexpr int STREAM_STAGE = 32 * 128;
 constexpr int stream_st(int nt) { return nt == 1 ? 4 : 3; }
 constexpr int stream_group(int nt) { return 1024 + 512 * nt; }  // the weights' scales, then x's
@@ -697,6 +703,18 @@ __global__ __launch_bounds__(KS == 1 ? 256 : 512, 2) void mx4_stream_kernel(Mx4A
 //
 // SG: scale rows are whole dwords apart and aligned, so that those 16 bytes can be
 // loaded directly; else they come byte by byte through registers.
+//
+// A stage of 256 rows takes 1.86 us on all CUs: its loads alone 1.65 (1.33 with more
+// room to wait for them), its products 1.33, its LDS reads 0.70, reads and products
+// 1.57.  4096 x 6144 x 7168 104 us, 3.5 PFLOP/s.  Slower: waves of 64 x 256 (119 for
+// 110), stages of 128 inputs four deep (2.09 for 1.86).  Of a pair, the 64 values a
+// lane of SiTU-GLU come on top, 9 of an item's 45 us at K = 3584: gate and up of 4096
+// tokens, four of 16 experts each, 291 us, without it 234; work-groups that stay and
+// request their next item before they write one need some 70 registers more than
+// there are (16384 tokens, two of 112 experts each: 815 us for 669).  With some 70 rows
+// an expert the weights are the bound, 3.9 TB/s with two stages of them on their way
+// (4096 tokens, two of 112 experts each: 337 us); tiles of half the size two on a CU
+// took 348, a dword of each row of the stage after asked for into the L2 358.
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 // c + 32 rows times 32 columns over 64 codes, scaled by byte J of each operand's scales

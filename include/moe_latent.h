@@ -542,7 +542,7 @@ typedef struct {
   const int32_t *sorted_pair;    /* [P], needed with top_k > 0 or pair_weight */
   const uint8_t *w, *w_scale;    /* [E, N, K/2], [E, N, K/32] */
   const uint8_t *w3, *w3_scale;  /* both or neither: out = SiTU-GLU(x w^T, x w3^T) */
-  float beta, beta_lin;          /* of SiTU-GLU */
+  float beta, beta_lin;          /* of SiTU-GLU, 2^-100 to 2^100 */
   const float *pair_weight;      /* sorted row p is scaled by pair_weight[sorted_pair[p]]; NULL: not; not with w3 */
   void *out;
   int64_t ldo;                   /* elements, >= N; MOE_DT_MXFP4: bytes, >= N/2 and a multiple of 16 */
@@ -561,10 +561,10 @@ typedef struct {
  * rows cost nothing; nothing waits on the host.  Device preconditions:
  * ascending offsets from 0 to at most P, sorted_pair[p] / top_k in [0, x_rows).
  * Deterministic.  Limits (else MOE_ENOTSUP): K a multiple of 32, N too with
- * MOE_DT_MXFP4; at most 1024 experts; P up to 2^21, N up to 2^18, K up to 2^20, P *
- * N up to 2^33, ldx and ldxs up to 2^22; gathered, x_rows * ldx and x_rows * ldxs
- * below 2^31.  P may
- * be 0.  Workspace: moe_mxfp4_expert_gemm_workspace_bytes(E, P, N, K) bytes (0:
+ * MOE_DT_MXFP4; both betas from 2^-100 to 2^100 with w3; at most 1024 experts; P
+ * up to 2^21, N up to 2^18, K up to 2^20, P * N up to 2^33, ldx and ldxs up to
+ * 2^22; gathered, x_rows * ldx and x_rows * ldxs below 2^31.  P may be 0.
+ * Workspace: moe_mxfp4_expert_gemm_workspace_bytes(E, P, N, K) bytes (0:
  * unsupported).
  * Errors: MOE_EINVAL, MOE_ENOTSUP, MOE_EWORKSPACE. */
 size_t moe_mxfp4_expert_gemm_workspace_bytes(int E, int P, int N, int K);

@@ -576,6 +576,8 @@ static int mxfp4_check_experts(int E, int P, int N, int K) {
   if (rc) return rc;
   return E > MX4_MAX_E || N > (1 << 18) ? MOE_ENOTSUP : MOE_OK;
 }
+// SiTU-GLU divides by its betas through their reciprocals: both far inside fp32's normal range
+static bool mxfp4_beta_ok(float b) { return b >= 0x1p-100f && b <= 0x1p100f; }
 // how rows of the result can be written: 16 bytes at a time, bf16 8, value by value
 static int rows_vec(const void *p, long long ld, int dtype) {
   const long long bytes = ld * (long long)dtype_bytes(dtype);
@@ -639,6 +641,7 @@ static int mxfp4_expert_impl(const moe_mxfp4_expert_args *a, void *ws, size_t ws
     return MOE_EINVAL;
   }
   if (a->ldx > (1 << 22) || a->ldxs > (1 << 22)) return MOE_ENOTSUP;
+  if (pair && !(mxfp4_beta_ok(a->beta) && mxfp4_beta_ok(a->beta_lin))) return MOE_ENOTSUP;
   // gathered rows are addressed with 32 bits from the first one
   if (gathered && (long long)a->x_rows * a->ldx >= (1LL << 31)) return MOE_ENOTSUP;
   if (gathered && (long long)a->x_rows * a->ldxs >= (1LL << 31)) return MOE_ENOTSUP;

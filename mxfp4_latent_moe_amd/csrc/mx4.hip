@@ -167,14 +167,16 @@ MOE_DEV void tanh_ratio(float x, float &num, float &den) {
   den = fmaf(q, t, 0.001953125f);
 }
 
-// SiTU-GLU of a tile's sums: 31 instructions a value where situ_glu has 43.  Denominators lie
+// SiTU-GLU of a tile's sums: 32 instructions a value where situ_glu has 43.  Denominators lie
 // between 2^-9 and 1, so that their product overflows where 1 + exp(-g) does (there the result is 0).
+// Each beta goes to its own fraction, as the product of the two may leave fp32's range, and the
+// reciprocal to the first, which it can only take to 0 and never from infinity to NaN.
 MOE_DEV float situ4(float g, float u, float beta, float beta_lin) {
   float ng, dg, nu, du;
   tanh_ratio(g * __builtin_amdgcn_rcpf(beta), ng, dg);
   tanh_ratio(u * __builtin_amdgcn_rcpf(beta_lin), nu, du);
   const float ds = 1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f);
-  return (ng * __builtin_amdgcn_rcpf(dg * du * ds)) * (nu * (beta * beta_lin));
+  return (beta * ng * __builtin_amdgcn_rcpf(dg * du * ds)) * (beta_lin * nu);
 }
 
 // an expert's rows [row, row + n) of a grouped product, or rows of the dense one

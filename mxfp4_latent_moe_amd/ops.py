@@ -348,7 +348,8 @@ def mxfp4_expert_gemm(x, x_scale, w, w_scale, offsets, out, ws, w3=None, w3_scal
     """The routed experts' products on MXFP4 rows (moe_mxfp4_expert_gemm): out [P, N], rows sorted by expert, expert e
     owning rows offsets[e] .. offsets[e + 1] (int32 [E + 1]; rows from offsets[E] on are left as they were).
     x [rows, K / 2] with x_scale [rows, K / 32]: row p itself, or with top_k row sorted_pair[p] // top_k.
-    w [E, N, K / 2] with w_scale [E, N, K / 32]; with w3 and w3_scale the result is SiTU-GLU of the two products.
+    w [E, N, K / 2] with w_scale [E, N, K / 32]; with w3 and w3_scale the result is SiTU-GLU of the two products
+    (beta and beta_lin from 2^-100 to 2^100).
     pair_weight (fp32, without w3): row p times pair_weight[sorted_pair[p]].  out is fp32, bf16, or with w3 MXFP4:
     codes [P, N / 2] with out_scale [P, N / 32].  ws holds mxfp4_expert_gemm_workspace_bytes(E, P, N, K) bytes."""
     dev = w.device

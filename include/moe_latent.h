@@ -559,7 +559,8 @@ typedef struct {
  * Products are exact, sums and SiTU-GLU fp32, other outputs rounded once.
  * Rows of out from expert_offsets[E] on are left as they were; experts without
  * rows cost nothing; nothing waits on the host.  Device preconditions:
- * ascending offsets from 0 to at most P, sorted_pair[p] / top_k in [0, x_rows).
+ * ascending offsets from 0 to at most P, sorted_pair[p] / top_k in [0, x_rows),
+ * sorted_pair[p] within pair_weight.
  * Deterministic.  Limits (else MOE_ENOTSUP): K a multiple of 32, N too with
  * MOE_DT_MXFP4; both betas from 2^-100 to 2^100 with w3; at most 1024 experts; P
  * up to 2^21, N up to 2^18, K up to 2^20, P * N up to 2^33, ldx and ldxs up to

@@ -350,8 +350,9 @@ def mxfp4_expert_gemm(x, x_scale, w, w_scale, offsets, out, ws, w3=None, w3_scal
     x [rows, K / 2] with x_scale [rows, K / 32]: row p itself, or with top_k row sorted_pair[p] // top_k.
     w [E, N, K / 2] with w_scale [E, N, K / 32]; with w3 and w3_scale the result is SiTU-GLU of the two products
     (beta and beta_lin from 2^-100 to 2^100).
-    pair_weight (fp32, without w3): row p times pair_weight[sorted_pair[p]].  out is fp32, bf16, or with w3 MXFP4:
-    codes [P, N / 2] with out_scale [P, N / 32].  ws holds mxfp4_expert_gemm_workspace_bytes(E, P, N, K) bytes."""
+    pair_weight (fp32, without w3): row p times pair_weight[sorted_pair[p]], a value for every pair (with top_k at least
+    rows * top_k).  out is fp32, bf16, or with w3 MXFP4: codes [P, N / 2] with out_scale [P, N / 32].  ws holds
+    mxfp4_expert_gemm_workspace_bytes(E, P, N, K) bytes."""
     dev = w.device
     if w.dim() != 3:
         raise ValueError(f"w: shape {tuple(w.shape)}, want [E, N, K / 2]")
@@ -372,8 +373,12 @@ def mxfp4_expert_gemm(x, x_scale, w, w_scale, offsets, out, ws, w3=None, w3_scal
     if sorted_pair is not None:
         a.sorted_pair = _vector("sorted_pair", sorted_pair, P, torch.int32, dev)
     if pair_weight is not None:
-        if pair_weight.dtype != torch.float32 or pair_weight.device != dev or not pair_weight.is_contiguous():
-            raise ValueError(f"pair_weight: want contiguous float32 on {dev}")
+        # every sorted_pair[p] that x's rows allow; without top_k they say nothing of the pairs
+        n = max(1, x.shape[0] * top_k)
+        if (pair_weight.dtype != torch.float32 or pair_weight.device != dev or not pair_weight.is_contiguous()
+                or pair_weight.numel() < n):
+            raise ValueError(f"pair_weight: {pair_weight.dtype} {tuple(pair_weight.shape)} on {pair_weight.device}, want "
+                             f"contiguous float32 on {dev}, at least {n} values")
         a.pair_weight = _p(pair_weight)
     if out_scale is not None:
         a.out_dtype, a.ldo = _lib.MOE_DT_MXFP4, _rows("out", out, (P, N // 2), _PACKED, dev)

@@ -125,10 +125,15 @@ _CODES = tuple(d for d in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) i
 _SCALES = tuple(d for d in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if d is not None)
 
 
+_MOST = 2 ** 31 - 1  # sizes are the library's ints: past them ctypes would pass their low bits on
+
+
 def _rows(name, t, shape, dtypes, device):
     """Leading dimension of a 2-d tensor whose rows are contiguous, after its checks."""
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
+    if max(shape) > _MOST:
+        raise ValueError(f"{name}: shape {tuple(shape)}, at most {_MOST} rows and values a row")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, want one of {tuple(dtypes)}")
     if t.device != device:
@@ -313,11 +318,15 @@ def mxfp4_dequantize(q, q_scale, out, stream=None):
 
 
 def mxfp4_gemm_workspace_bytes(T: int, N: int, K: int) -> int:
+    if max(T, N, K) > _MOST:
+        return 0
     return int(load().moe_mxfp4_gemm_workspace_bytes(T, N, K))
 
 
 def _stack(name, t, shape, dtypes, device):
     """The pointer of a contiguous weight tensor, after its checks."""
+    if max(shape) > _MOST // 2:
+        raise ValueError(f"{name}: shape {shape}, at most {_MOST // 2} values")
     if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, want contiguous {shape} on {device}, "
                          f"one of {dtypes}")
@@ -340,6 +349,8 @@ def mxfp4_gemm(x, x_scale, w, w_scale, out, ws, accumulate=False, stream=None):
 
 
 def mxfp4_expert_gemm_workspace_bytes(E: int, P: int, N: int, K: int) -> int:
+    if max(E, P, N, K) > _MOST:
+        return 0
     return int(load().moe_mxfp4_expert_gemm_workspace_bytes(E, P, N, K))
 
 
@@ -356,6 +367,8 @@ def mxfp4_expert_gemm(x, x_scale, w, w_scale, offsets, out, ws, w3=None, w3_scal
     dev = w.device
     if w.dim() != 3:
         raise ValueError(f"w: shape {tuple(w.shape)}, want [E, N, K / 2]")
+    if not 0 <= top_k <= _MOST:
+        raise ValueError(f"top_k: {top_k}")
     E, N, K = w.shape[0], w.shape[1], 2 * w.shape[2]
     P = out.shape[0]
     a = _lib.MoeMxfp4ExpertArgs()

@@ -32,3 +32,35 @@ def test_pair_weight():
     for args in ((20, 30, (40,), 2), (20, 30, (20, 2), 2), (20, 30, (41,), 2), (30, 30, (30,), 0), (30, 30, (7,), 0)):
         with pytest.raises(ValueError, match=NOT_ON_GPU):
             down(*args)
+
+
+BIG = 2 ** 32 + 5  # five, to a call that keeps the low 32 bits
+
+
+def test_sizes_past_32_bits():
+    """Sizes that the library's ints cannot hold are refused, not cut to their low bits."""
+    f32 = torch.float32
+    calls = [
+        lambda: mx.mxfp4_quantize(meta(BIG, 1, dtype=f32), meta(BIG, 1), meta(BIG, 1)),
+        lambda: mx.mxfp4_quantize(meta(1, BIG, dtype=f32), meta(1, BIG // 2 + 1), meta(1, BIG // 32 + 1)),
+        lambda: mx.mxfp4_dequantize(meta(BIG, 1), meta(BIG, 1), meta(BIG, 1, dtype=f32)),
+        lambda: mx.mxfp4_gemm(meta(BIG, 16), meta(BIG, 1), meta(1, 16), meta(1, 1), meta(BIG, 1, dtype=f32), meta(1024)),
+        lambda: mx.mxfp4_gemm(meta(1, 16), meta(1, 1), meta(BIG, 16), meta(BIG, 1), meta(1, BIG, dtype=f32), meta(1024)),
+        lambda: mx.mxfp4_gemm(meta(1, 2 ** 31 + 16), meta(1, 2 ** 27 + 1), meta(1, 2 ** 31 + 16), meta(1, 2 ** 27 + 1),
+                              meta(1, 1, dtype=f32), meta(1024)),
+        lambda: mx.mxfp4_expert_gemm(meta(BIG, 16), meta(BIG, 1), meta(1, 1, 16), meta(1, 1, 1), meta(2, dtype=torch.int32),
+                                     meta(4, 1, dtype=f32), meta(1024)),
+        lambda: mx.mxfp4_expert_gemm(meta(9, 16), meta(9, 1), meta(1, 1, 16), meta(1, 1, 1), meta(2, dtype=torch.int32),
+                                     meta(BIG, 1, dtype=f32), meta(1024)),
+        lambda: mx.mxfp4_expert_gemm(meta(9, 16), meta(9, 1), meta(BIG, 1, 16), meta(BIG, 1, 1),
+                                     meta(BIG + 1, dtype=torch.int32), meta(4, 1, dtype=f32), meta(1024)),
+        lambda: mx.mxfp4_expert_gemm(meta(9, 16), meta(9, 1), meta(1, 1, 16), meta(1, 1, 1), meta(2, dtype=torch.int32),
+                                     meta(4, 1, dtype=f32), meta(1024), sorted_pair=meta(4, dtype=torch.int32), top_k=BIG),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError) as e:
+            call()
+        assert NOT_ON_GPU not in str(e.value), i
+    assert mx.mxfp4_gemm_workspace_bytes(BIG, 32, 32) == mx.mxfp4_gemm_workspace_bytes(32, BIG, 32) == 0
+    for sizes in ((BIG, 32, 32, 32), (32, BIG, 32, 32), (32, 32, BIG, 32), (32, 32, 32, 2 ** 32 + 32)):
+        assert mx.mxfp4_expert_gemm_workspace_bytes(*sizes) == 0

@@ -728,7 +728,7 @@ MOE_DEV f32x16_t mfma_4_32(u32x4_t w, u32x4_t x, f32x16_t c, uint32_t sw, uint32
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, J, (int)sw, J, (int)sx);
 }
 
-constexpr int TILE_ROWS = 256;    // rows of x
+constexpr int TILE_ROWS = MX4_TILE_ROWS;  // rows of x
 constexpr int TILE_COLS = 256;    // weight rows
 constexpr int GROUP_BYTES = (TILE_COLS + TILE_ROWS) * 16;  // scales of two stages
 constexpr int stages_of(int nt) { return nt <= 2 ? 3 : 2; }
@@ -1197,21 +1197,6 @@ void launch_tiles(const Mx4Args &g, long long groups, int rows, int cut, int spl
 }
 long long up8(long long v) { return (v + 7) / 8 * 8; }
 
-// An expert's rows up to which its weights are streamed by waves of their own.  The down product of 256
-// tokens over 64 experts, four each, uneven: 61 us at 16, 61 at 8, 68 at 24, 69 at 32; gate and up of 64
-// tokens 94, 91, 101, 105; of 1024 tokens, two each, 168, 169, 188, 184.
-// With 32 rows an expert on average and more, tiles take them all, as the few that the others would have are
-// not worth a launch behind them: of 4096 tokens, two of 112 experts each, gate and up 339 with both, 330 with
-// tiles alone, down 191 and 184; of 1024 tokens, two of 64 each, down 116 and 100 (with experts' weights e^1.5
-// apart, the rows with a few of them, 67 and 71).
-int few_rows(int E, int P) { return P >= 32LL * E ? 0 : 16; }
-int few_chunks(int E, int P) { return few_rows(E, P) > 0 ? std::min(E, P) : 0; }
-int many_chunks(int E, int P) { return P / TILE_ROWS + std::min(E, P / (few_rows(E, P) + 1)); }
-// work-groups of the stream kernel for a chunk
-int stream_groups(const Mx4Args &g) {
-  const int cols = g.w[1] != nullptr ? 64 : 128;
-  return (g.N + cols - 1) / cols;
-}
 }  // namespace
 
 size_t mx4_workspace_bytes(int T, int N, int K) { return mx4_partial_bytes(T, N, K); }
@@ -1240,37 +1225,36 @@ hipError_t launch_mx4_gemm(const Mx4Args &g, void *ws, hipStream_t st) {
 }
 
 size_t mx4_expert_workspace_bytes(int E, int P, int, int) {
-  return 256 + (size_t)(few_chunks(E, P) + many_chunks(E, P)) * sizeof(int4);
+  return 256 + (size_t)(mx4_few_chunks(E, P) + mx4_many_chunks(E, P)) * sizeof(int4);
 }
 
 hipError_t launch_mx4_expert(const Mx4Args &a, void *ws, hipStream_t st) {
   Mx4Args g = a;
-  const int E = g.n_experts, groups = stream_groups(g);
+  const int E = g.n_experts, groups = mx4_stream_groups(g.N, g.w[1] != nullptr);
   const bool pair = g.w[1] != nullptr;
-  // few work-groups: they look for their chunks themselves, in place of a launch before
-  const int chunks = g.P / 64 + std::min(E, g.P);
-  if ((long long)chunks * groups <= 1024) {
+  if (mx4_finds_chunks(E, g.P, groups)) {
+    const int chunks = mx4_found_chunks(E, g.P);
     if (pair) launch_stream<4, true, 1>(g, (long long)chunks * groups, st);
     else launch_stream<4, false, 1>(g, (long long)chunks * groups, st);
     return hipGetLastError();
   }
   int32_t *count = static_cast<int32_t *>(ws);
-  int4 *few = reinterpret_cast<int4 *>(static_cast<char *>(ws) + 256), *many = few + few_chunks(E, g.P);
-  hipLaunchKernelGGL(mx4_plan_kernel, dim3(1), dim3(1024), 0, st, g.offsets, E, g.P, few_rows(E, g.P), TILE_ROWS,
-                     few_chunks(E, g.P), few, count, many_chunks(E, g.P), many, count + 1);
+  int4 *few = reinterpret_cast<int4 *>(static_cast<char *>(ws) + 256), *many = few + mx4_few_chunks(E, g.P);
+  hipLaunchKernelGGL(mx4_plan_kernel, dim3(1), dim3(1024), 0, st, g.offsets, E, g.P, mx4_few_rows(E, g.P), TILE_ROWS,
+                     mx4_few_chunks(E, g.P), few, count, mx4_many_chunks(E, g.P), many, count + 1);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (many_chunks(E, g.P) > 0) {
+  if (mx4_many_chunks(E, g.P) > 0) {
     g.chunks = many;
     g.chunk_count = count + 1;
-    launch_tiles(g, up8((long long)many_chunks(E, g.P) * ((g.N + (pair ? 127 : 255)) / (pair ? 128 : 256))), 0, 0, 1, nullptr, st);
+    launch_tiles(g, up8((long long)mx4_many_chunks(E, g.P) * ((g.N + (pair ? 127 : 255)) / (pair ? 128 : 256))), 0, 0, 1, nullptr, st);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (few_chunks(E, g.P) == 0) return hipSuccess;
+  if (mx4_few_chunks(E, g.P) == 0) return hipSuccess;
   g.chunks = few;
   g.chunk_count = count;
-  if (pair) launch_stream<1, true, 1>(g, (long long)few_chunks(E, g.P) * groups, st);
-  else launch_stream<1, false, 1>(g, (long long)few_chunks(E, g.P) * groups, st);
+  if (pair) launch_stream<1, true, 1>(g, (long long)mx4_few_chunks(E, g.P) * groups, st);
+  else launch_stream<1, false, 1>(g, (long long)mx4_few_chunks(E, g.P) * groups, st);
   return hipGetLastError();
 }
 

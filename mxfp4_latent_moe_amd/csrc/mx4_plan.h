@@ -1,5 +1,5 @@
-// Which kernel of the dense MXFP4 product runs, and how it is cut: host code
-// alone, a function of the sizes.
+// Which kernels of the MXFP4 products run, and how they are cut: host code alone, a
+// function of the sizes.
 #pragma once
 #include <stddef.h>
 
@@ -77,5 +77,25 @@ inline size_t mx4_partial_bytes(int T, int N, int K) {
   const Mx4Plan p = mx4_plan(T, N, K);
   return !p.stream && p.splits > 1 ? (size_t)p.splits * T * ((N + 3) / 4) * 16 : 0;
 }
+
+// ---- expert products
+constexpr int MX4_TILE_ROWS = 256;  // rows of a tile, at most
+
+// An expert's rows up to which its weights are streamed by waves of their own.  The down product of 256
+// tokens over 64 experts, four each, uneven: 61 us at 16, 61 at 8, 68 at 24, 69 at 32; gate and up of 64
+// tokens 94, 91, 101, 105; of 1024 tokens, two each, 168, 169, 188, 184.
+// With 32 rows an expert on average and more, tiles take them all, as the few that the others would have are
+// not worth a launch behind them: of 4096 tokens, two of 112 experts each, gate and up 339 with both, 330 with
+// tiles alone, down 191 and 184; of 1024 tokens, two of 64 each, down 116 and 100 (with experts' weights e^1.5
+// apart, the rows with a few of them, 67 and 71).
+inline int mx4_few_rows(int E, int P) { return P >= 32LL * E ? 0 : 16; }
+inline int mx4_few_chunks(int E, int P) { return mx4_few_rows(E, P) > 0 ? std::min(E, P) : 0; }
+inline int mx4_many_chunks(int E, int P) { return P / MX4_TILE_ROWS + std::min(E, P / (mx4_few_rows(E, P) + 1)); }
+// work-groups of the stream kernel for a chunk
+inline int mx4_stream_groups(int N, bool pair) { return (N + (pair ? 63 : 127)) / (pair ? 64 : 128); }
+// chunks of up to 64 rows, at most, of work-groups that look for them themselves
+inline int mx4_found_chunks(int E, int P) { return P / 64 + std::min(E, P); }
+// few work-groups: they do so, in place of a launch before
+inline bool mx4_finds_chunks(int E, int P, int groups) { return (long long)mx4_found_chunks(E, P) * groups <= 1024; }
 
 }  // namespace moe

@@ -519,7 +519,8 @@ int moe_mxfp4_dequantize(int T, int K, const uint8_t *q, int64_t ldq, const uint
  *   out     [T, ldo]  fp32 (written, or added to with accumulate = 1) or bf16
  * Products are exact and sums fp32 in both outputs; bf16 is rounded once.  Scale
  * bytes are 0..254; 255 gives NaN in its row or column.  Where the product of a
- * block's two scales leaves fp32's range the result is unspecified.
+ * block's two scales leaves fp32's range the result is unspecified, but for
+ * blocks of zeros, which add nothing under any two scales.
  * Deterministic.  T may be 0; N is free; K is a multiple of 32 (else
  * MOE_ENOTSUP; T up to 2^21, N and K up to 2^20, T * N up to 2^33, ldx and ldxs up
  * to 2^22).

@@ -245,3 +245,32 @@ def test_expert_many_experts(mx):
     say("case: expert products, direct scales, 1024 experts")
     routed(mx, counts, 128, 384, True, "mx4", True)
     routed(mx, counts, 129, 384, False, "f32", False, True, pitch=4)
+
+
+@pytest.mark.parametrize("T,N", [(16, 300), (20, 300), (300, 1300), (700, 6200)])
+def test_blocks_of_zeros(mx, T, N):
+    """Blocks of zeros add nothing, under scales whose product is far outside fp32's range too: quantised zeros have the
+    least scale there is, 2^-125, and weights are below 1."""
+    K = 512
+    say(f"case: 4-bit product of blocks of zeros, T={T} N={N}")
+    g = seeded(T)
+    rows = torch.randn(T, K, generator=g, device=DEV)
+    rows[:, :128] = 0
+    rows[0] = 0
+    x, xs = (torch.empty((T, n), dtype=torch.uint8, device=DEV) for n in (K // 2, K // 32))
+    mx.mxfp4_quantize(rows, x, xs)
+    assert (xs[:, :4] == 2).all() and (xs[0] == 2).all()
+    w, ws = codes(g, N, K // 2), scales(g, 118, N, K // 32)
+    # under the rows' zeros (blocks 0 to 3) weights of every scale; under zeros of both signs in the weights (4 to 7) rows
+    ws[:, :4] = torch.randint(0, 255, (N, 4), generator=g, device=DEV).byte()
+    w[:, 64:128] &= 0x88
+    ws[:, 4:8] = torch.randint(0, 255, (N, 4), generator=g, device=DEV).byte()
+    xs[1:, 4:8] = torch.randint(0, 255, (T - 1, 4), generator=g, device=DEV).byte()
+    ws[0, :8], xs[1, 4:8], ws[1, :8], xs[2, 4:8] = 254, 254, 0, 0
+    out = torch.empty((T, N), device=DEV)
+    mx.mxfp4_gemm(x, xs, w, ws, out, workspace(mx.mxfp4_gemm_workspace_bytes(T, N, K)))
+    a, b = values(x, xs), values(w, ws)
+    ref, mag = a @ b.T.contiguous(), a.abs() @ b.abs().T.contiguous()
+    assert torch.isfinite(out).all() and (out[0] == 0).all()
+    # 128 additions in an instruction, K / 64 instructions, 16 joins, each off by 2^-23 of the sum of magnitudes at most
+    assert ((out.double() - ref).abs() <= (128 + K // 64 + 16) * 2.0 ** -23 * mag).all()

@@ -6,6 +6,7 @@ import subprocess
 
 import pytest
 from test_gpu_mx4_direct import DENSE, EXPERTS, LONG
+from test_gpu_mx4_layer_lists import BOTH, TILES, WIDE
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "mxfp4_latent_moe_amd", "csrc")
 MAIN = r"""
@@ -104,3 +105,11 @@ def test_lists_hold_every_chunk(plan):
                     assert sum(-(-n // 256) for n in c if n > few) <= many_cap
             assert groups * (found if finds else few_cap) * 256 < 2 ** 32
             assert -(-N // (128 if kind == "p" else 256)) * many_cap * 512 < 2 ** 32
+
+
+def test_layer_sizes(plan):
+    """The layer test's token counts: lists for both products, on either side of 32 rows an expert."""
+    for T, few in ((BOTH, 16), (TILES, 0)):
+        for kind, N in (("p", WIDE.inter), ("s", WIDE.latent)):
+            [(finds, _, _, few_rows, _, many)] = plan(kind, [(WIDE.n_experts, T * WIDE.top_k, N)])
+            assert not finds and few_rows == few and many > 0

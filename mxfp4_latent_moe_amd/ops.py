@@ -125,15 +125,17 @@ _CODES = tuple(d for d in (torch.uint8, getattr(torch, "float8_e4m3fn", None)) i
 _SCALES = tuple(d for d in (torch.uint8, getattr(torch, "float8_e8m0fnu", None)) if d is not None)
 
 
-_MOST = 2 ** 31 - 1  # sizes are the library's ints: past them ctypes would pass their low bits on
+_MOST = 2 ** 31 - 1  # sizes are the library's ints: ctypes would pass the low bits of larger ones on
+
+
+def _too_large(name):
+    raise ValueError(f"{name}: sizes of at most {_MOST}")
 
 
 def _rows(name, t, shape, dtypes, device):
     """Leading dimension of a 2-d tensor whose rows are contiguous, after its checks."""
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, want {tuple(shape)}")
-    if max(shape) > _MOST:
-        raise ValueError(f"{name}: shape {tuple(shape)}, at most {_MOST} rows and values a row")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, want one of {tuple(dtypes)}")
     if t.device != device:
@@ -199,6 +201,8 @@ def block_pre_norm(x, gamma, eps=1e-6, n=None, q=None, q_scale=None, stream=None
     """RMSNorm in front of a block (moe_block_pre_norm): x [T, H] fp32 or bf16, written as bf16 to n and / or as
     e4m3 codes to q with a scale byte per 128 channels to q_scale.  Rows may be strided."""
     T, H = x.shape
+    if T > _MOST or H > _MOST:
+        _too_large("block_pre_norm")
     ldx = _rows("x", x, (T, H), _FLOATS, x.device)
     o = _norm_out(T, H, x.device, gamma, n, q, q_scale)
     if T == 0:
@@ -213,6 +217,8 @@ def block_post_norm(y, resid, out, gamma=None, gate=None, gate_sigmoid=False, sc
     tensor of shape [T, 1], [1, H] or [T, H]; a [1, 1] gate of a single row is one value for it.  out may be resid.
     next_gamma with n and / or q and q_scale: RMSNorm of out as stored."""
     T, H = resid.shape
+    if T > _MOST or H > _MOST:
+        _too_large("block_post_norm")
     dev = resid.device
     a = _lib.MoePostNormArgs()
     a.T, a.H, a.scale, a.eps, a.gate_sigmoid = T, H, scale, eps, int(gate_sigmoid)
@@ -250,6 +256,8 @@ def fp8_quantize(x, q, q_scale, stream=None):
     """Rows of x [T, K] (fp32 or bf16) as e4m3 codes q [T, K] with a scale byte per 128 values q_scale
     [T, ceil(K / 128)] (moe_fp8_quantize)."""
     T, K = x.shape
+    if T > _MOST or K > _MOST:
+        _too_large("fp8_quantize")
     ldx = _rows("x", x, (T, K), _FLOATS, x.device)
     ldq = _rows("q", q, (T, K), _CODES, x.device)
     lds = _rows("q_scale", q_scale, (T, -(-K // 128)), _SCALES, x.device)
@@ -268,6 +276,8 @@ def fp8_gemm(x, x_scale, w, w_scale, out, ws, accumulate=False, stream=None):
     out is fp32 or bf16; ws holds fp8_gemm_workspace_bytes(T, N, K) bytes."""
     T, K = x.shape
     N = w.shape[0]
+    if T > _MOST or N > _MOST or K > _MOST:
+        _too_large("fp8_gemm")
     kb = -(-K // 128)
     dev = w.device
     ldx = _rows("x", x, (T, K), _CODES, dev)
@@ -294,6 +304,8 @@ def mxfp4_quantize(x, q, q_scale, rule="fit", stream=None):
     byte b's low nibble, and scale bytes q_scale [T, ceil(K / 32)].  rule "fit": the smallest power-of-two scale with
     which nothing saturates; "ocp": the MX format's own, by the largest magnitude's exponent."""
     T, K = x.shape
+    if T > _MOST or K > _MOST:
+        _too_large("mxfp4_quantize")
     if rule not in _RULES:
         raise ValueError(f"rule: {rule!r}, want one of {tuple(_RULES)}")
     ldx = _rows("x", x, (T, K), _FLOATS, x.device)
@@ -308,6 +320,8 @@ def mxfp4_quantize(x, q, q_scale, rule="fit", stream=None):
 def mxfp4_dequantize(q, q_scale, out, stream=None):
     """MXFP4 rows (see mxfp4_quantize) as values: out [T, K] fp32 or bf16 (moe_mxfp4_dequantize)."""
     T, K = out.shape
+    if T > _MOST or K > _MOST:
+        _too_large("mxfp4_dequantize")
     ldq = _rows("q", q, (T, -(-K // 2)), _PACKED, out.device)
     lds = _rows("q_scale", q_scale, (T, -(-K // 32)), _SCALES, out.device)
     ldo = _rows("out", out, (T, K), _FLOATS, out.device)
@@ -325,8 +339,6 @@ def mxfp4_gemm_workspace_bytes(T: int, N: int, K: int) -> int:
 
 def _stack(name, t, shape, dtypes, device):
     """The pointer of a contiguous weight tensor, after its checks."""
-    if max(shape) > _MOST // 2:
-        raise ValueError(f"{name}: shape {shape}, at most {_MOST // 2} values")
     if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, want contiguous {shape} on {device}, "
                          f"one of {dtypes}")
@@ -338,6 +350,8 @@ def mxfp4_gemm(x, x_scale, w, w_scale, out, ws, accumulate=False, stream=None):
     (see mxfp4_quantize), w [N, K / 2] with w_scale [N, K / 32].  out is fp32 or bf16; ws holds
     mxfp4_gemm_workspace_bytes(T, N, K) bytes."""
     (T, N), K, dev = out.shape, 2 * w.shape[-1], w.device
+    if T > _MOST or N > _MOST or K > _MOST:
+        _too_large("mxfp4_gemm")
     ldx = _rows("x", x, (T, K // 2), _PACKED, dev)
     lds = _rows("x_scale", x_scale, (T, K // 32), _SCALES, dev)
     pw, pws = _stack("w", w, (N, K // 2), _PACKED, dev), _stack("w_scale", w_scale, (N, K // 32), _SCALES, dev)
@@ -367,15 +381,15 @@ def mxfp4_expert_gemm(x, x_scale, w, w_scale, offsets, out, ws, w3=None, w3_scal
     dev = w.device
     if w.dim() != 3:
         raise ValueError(f"w: shape {tuple(w.shape)}, want [E, N, K / 2]")
-    if not 0 <= top_k <= _MOST:
-        raise ValueError(f"top_k: {top_k}")
-    E, N, K = w.shape[0], w.shape[1], 2 * w.shape[2]
-    P = out.shape[0]
+    E, N, K = w.shape
+    P, K, rows = out.shape[0], 2 * K, x.shape[0]
+    if P > _MOST or rows > _MOST or top_k > _MOST or E > _MOST or N > _MOST or K > _MOST:
+        _too_large("mxfp4_expert_gemm")
     a = _lib.MoeMxfp4ExpertArgs()
-    a.n_experts, a.P, a.N, a.K, a.top_k, a.x_rows = E, P, N, K, top_k, x.shape[0]
+    a.n_experts, a.P, a.N, a.K, a.top_k, a.x_rows = E, P, N, K, top_k, rows
     a.beta, a.beta_lin = beta, beta_lin
-    a.x, a.ldx = _p(x), _rows("x", x, (x.shape[0], K // 2), _PACKED, dev)
-    a.x_scale, a.ldxs = _p(x_scale), _rows("x_scale", x_scale, (x.shape[0], K // 32), _SCALES, dev)
+    a.x, a.ldx = _p(x), _rows("x", x, (rows, K // 2), _PACKED, dev)
+    a.x_scale, a.ldxs = _p(x_scale), _rows("x_scale", x_scale, (rows, K // 32), _SCALES, dev)
     a.w, a.w_scale = _stack("w", w, (E, N, K // 2), _PACKED, dev), _stack("w_scale", w_scale, (E, N, K // 32), _SCALES, dev)
     if (w3 is None) != (w3_scale is None):
         raise ValueError("w3 and w3_scale go together")
@@ -387,7 +401,7 @@ def mxfp4_expert_gemm(x, x_scale, w, w_scale, offsets, out, ws, w3=None, w3_scal
         a.sorted_pair = _vector("sorted_pair", sorted_pair, P, torch.int32, dev)
     if pair_weight is not None:
         # every sorted_pair[p] that x's rows allow; without top_k they say nothing of the pairs
-        n = max(1, x.shape[0] * top_k)
+        n = max(1, rows * top_k)
         if (pair_weight.dtype != torch.float32 or pair_weight.device != dev or not pair_weight.is_contiguous()
                 or pair_weight.numel() < n):
             raise ValueError(f"pair_weight: {pair_weight.dtype} {tuple(pair_weight.shape)} on {pair_weight.device}, want "

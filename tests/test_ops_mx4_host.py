@@ -39,8 +39,12 @@ BIG = 2 ** 32 + 5  # five, to a call that keeps the low 32 bits
 
 def test_sizes_past_32_bits():
     """Sizes that the library's ints cannot hold are refused, not cut to their low bits."""
-    f32 = torch.float32
+    f32, bf16 = torch.float32, torch.bfloat16
     calls = [
+        lambda: mx.block_pre_norm(meta(BIG, 1, dtype=f32), meta(1, dtype=bf16), n=meta(BIG, 1, dtype=bf16)),
+        lambda: mx.block_post_norm(meta(BIG, 1, dtype=f32), meta(BIG, 1, dtype=f32), meta(BIG, 1, dtype=f32)),
+        lambda: mx.fp8_quantize(meta(BIG, 1, dtype=f32), meta(BIG, 1), meta(BIG, 1)),
+        lambda: mx.fp8_gemm(meta(BIG, 1), meta(BIG, 1), meta(1, 1), meta(1, 1), meta(BIG, 1, dtype=f32), meta(1024)),
         lambda: mx.mxfp4_quantize(meta(BIG, 1, dtype=f32), meta(BIG, 1), meta(BIG, 1)),
         lambda: mx.mxfp4_quantize(meta(1, BIG, dtype=f32), meta(1, BIG // 2 + 1), meta(1, BIG // 32 + 1)),
         lambda: mx.mxfp4_dequantize(meta(BIG, 1), meta(BIG, 1), meta(BIG, 1, dtype=f32)),
@@ -55,7 +59,7 @@ def test_sizes_past_32_bits():
         lambda: mx.mxfp4_expert_gemm(meta(9, 16), meta(9, 1), meta(BIG, 1, 16), meta(BIG, 1, 1),
                                      meta(BIG + 1, dtype=torch.int32), meta(4, 1, dtype=f32), meta(1024)),
         lambda: mx.mxfp4_expert_gemm(meta(9, 16), meta(9, 1), meta(1, 1, 16), meta(1, 1, 1), meta(2, dtype=torch.int32),
-                                     meta(4, 1, dtype=f32), meta(1024), sorted_pair=meta(4, dtype=torch.int32), top_k=BIG),
+                                     meta(4, 1, dtype=f32), meta(1024), sorted_pair=meta(4, dtype=torch.int32), top_k=2 ** 32 + 1),
     ]
     for i, call in enumerate(calls):
         with pytest.raises(ValueError) as e:

@@ -353,12 +353,14 @@ MOE_DEV bool find_chunk(const Mx4Args &g, int rows, int want, Chunk &c, int *lds
 // Loads of two bytes a lane cost as much as those of sixteen.  With SG (scale rows
 // are whole dwords apart and aligned) the scales of two stages come into LDS by one
 // direct load for 32 rows, 16 bytes a row; without it byte by byte to registers
-// (39 us in place of 31 at 16 tokens, 7168 x 33792).
+// (16 tokens, 7168 x 33792: 39 us in place of 31 with x's scale rows strided; K of
+// 33824, whose scale rows are no whole dwords, 47).
 //
 // Bound by the weights.  One token: 3584 x 7168 5.9 us, 7168 x 33792 25 us, 5.1 TB/s;
 // 16 tokens 31 us, 4.2 TB/s, where half as many bytes of x as of weights come to a
 // CU.  Gate and up of one token's 16 experts 41 us, 4.5 TB/s; of 16 tokens through 896
-// experts (some 224 of them in use) 440 us, 5.9 TB/s, down 220 to 245.
+// experts (some 230 of them in use) 425 to 440 us, 6.1 TB/s, down 211 to 218 (505 and
+// 248 in a process that had allocated and freed other large weights before).
 constexpr int STREAM_STAGE = 32 * 128;
 constexpr int stream_st(int nt) { return nt == 1 ? 4 : 3; }
 constexpr int stream_group(int nt) { return 1024 + 512 * nt; }  // the weights' scales, then x's
@@ -704,11 +706,15 @@ __global__ __launch_bounds__(KS == 1 ? 256 : 512, 2) void mx4_stream_kernel(Mx4A
 // byte j.  Scales come into LDS 16 bytes a row, two stages at a time.
 //
 // SG: scale rows are whole dwords apart and aligned, so that those 16 bytes can be
-// loaded directly; else they come byte by byte through registers.
+// loaded directly; else they come byte by byte through registers: 16 loads of a byte a
+// lane for two stages, and one register spilled for a pair, two without.  So K whose
+// blocks are no multiple of four is slow: 4096 x 6144 x 7200 180 us where 7168 takes
+// 109, K = 2880 70 where 2816 takes 49, gate and up of 16384 tokens, two of 112 experts
+// each, 934 at K = 3616 for 614 at 3584.
 //
 // A stage of 256 rows takes 1.86 us on all CUs: its loads alone 1.65 (1.33 with more
 // room to wait for them), its products 1.33, its LDS reads 0.70, reads and products
-// 1.57.  4096 x 6144 x 7168 104 us, 3.5 PFLOP/s.  Slower: waves of 64 x 256 (119 for
+// 1.57.  4096 x 6144 x 7168 101 to 116 us with the card's clock, 3.1 to 3.6 PFLOP/s.  Slower: waves of 64 x 256 (119 for
 // 110), stages of 128 inputs four deep (2.09 for 1.86).  Of a pair, the 64 values a
 // lane of SiTU-GLU come on top, 9 of an item's 45 us at K = 3584: gate and up of 4096
 // tokens, four of 16 experts each, 291 us, without it 234; work-groups that stay and

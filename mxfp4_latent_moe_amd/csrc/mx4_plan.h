@@ -95,7 +95,15 @@ inline int mx4_many_chunks(int E, int P) { return P / MX4_TILE_ROWS + std::min(E
 inline int mx4_stream_groups(int N, bool pair) { return (N + (pair ? 63 : 127)) / (pair ? 64 : 128); }
 // chunks of up to 64 rows, at most, of work-groups that look for them themselves
 inline int mx4_found_chunks(int E, int P) { return P / 64 + std::min(E, P); }
-// few work-groups: they do so, in place of a launch before
+// Few work-groups do so, in place of a launch before, and stream whatever rows an expert has.  That saves the list
+// and, at decode, an empty launch, and loses where experts have many rows, as their weights are read once for every
+// 64.  Both sides at the layer's sizes (gate and up / down), experts x rows each, us, found / listed: 1 x 1 10 / 13,
+// 8 / 11; 16 x 1 42 / 40, 21 / 24; 8 x 16 26 / 31, 14 / 18; 16 x 16 44 / 47, 25 / 29; 4 x 32 19 / 23, 14 / 17; 1 x 256
+// 25 / 37, 20 / 28.  Lost: 4 x 64 29 / 24, 21 / 17; 4 x 128 45 / 29, 22 / 21; 8 x 64 50 / 29, 25 / 23; 4 x 256 62 / 42,
+// 36 / 31.  Past 1024 work-groups: 16 x 32 54 / 52, 30 / 29; 16 x 64 77 / 54, 42 / 31; 4 x 512 113 / 45, 65 / 36.  Small
+// layers: 32 x 32 of 128 x 128 6.9 / 10.1, 5.7 / 9.3, of 768 x 512 11.5 / 12.8, 8.0 / 10.9; 8 x 256 of 768 x 512
+// 16 / 22, 11 / 16; past 1024, 32 x 128 of 768 x 512 25 / 17, 15 / 15.  A rule on rows an expert would take lists from
+// some 64 of them in four experts and more where the weights are large.
 inline bool mx4_finds_chunks(int E, int P, int groups) { return (long long)mx4_found_chunks(E, P) * groups <= 1024; }
 
 }  // namespace moe

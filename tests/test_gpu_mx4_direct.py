@@ -274,3 +274,32 @@ def test_blocks_of_zeros(mx, T, N):
     assert torch.isfinite(out).all() and (out[0] == 0).all()
     # 128 additions in an instruction, K / 64 instructions, 16 joins, each off by 2^-23 of the sum of magnitudes at most
     assert ((out.double() - ref).abs() <= (128 + K // 64 + 16) * 2.0 ** -23 * mag).all()
+
+
+def test_element_types(mx):
+    """Codes and scales in torch's own types for them, where it has them, are the same bytes."""
+    if not hasattr(torch, "float4_e2m1fn_x2") or not hasattr(torch, "float8_e8m0fnu"):
+        pytest.skip("torch without 4-bit floats")
+    say("case: 4-bit products of tensors of torch's 4-bit and scale types")
+    four, e8 = (lambda t: t.view(torch.float4_e2m1fn_x2)), (lambda t: t.view(torch.float8_e8m0fnu))
+    g = seeded(4)
+    E, T, N, K = 3, 40, 96, 256
+    x, xs = torch.empty((T, K // 2), dtype=torch.uint8, device=DEV), torch.empty((T, K // 32), dtype=torch.uint8, device=DEV)
+    rows = torch.randn(T, K, generator=g, device=DEV)
+    mx.mxfp4_quantize(rows, four(x), e8(xs))
+    back, want = torch.empty_like(rows), values(x, xs)
+    mx.mxfp4_dequantize(four(x), e8(xs), back)
+    assert torch.equal(back.double(), want) and not torch.equal(want, torch.zeros_like(want))
+    w, ws, w3, ws3 = codes(g, E, N, K // 2), scales(g, 117, E, N, K // 32), codes(g, E, N, K // 2), scales(g, 117, E, N, K // 32)
+    scratch = workspace(1 << 16)
+    outs = [torch.empty((T, N), device=DEV) for _ in range(2)]
+    mx.mxfp4_gemm(x, xs, w[0], ws[0], outs[0], scratch)
+    mx.mxfp4_gemm(four(x), e8(xs), four(w[0]), e8(ws[0]), outs[1], scratch)
+    assert torch.equal(*outs)
+    off = torch.tensor([0, 7, 7, T], dtype=torch.int32, device=DEV)
+    h = [(torch.zeros((T, N // 2), dtype=torch.uint8, device=DEV), torch.zeros((T, N // 32), dtype=torch.uint8, device=DEV))
+         for _ in range(2)]
+    mx.mxfp4_expert_gemm(x, xs, w, ws, off, h[0][0], scratch, w3=w3, w3_scale=ws3, out_scale=h[0][1])
+    mx.mxfp4_expert_gemm(four(x), e8(xs), four(w), e8(ws), off, four(h[1][0]), scratch, w3=four(w3), w3_scale=e8(ws3),
+                         out_scale=e8(h[1][1]))
+    assert torch.equal(h[0][0], h[1][0]) and torch.equal(h[0][1], h[1][1]) and h[0][0].any()
